@@ -313,3 +313,17 @@ def fp4q_decompress_mx(codes, scales, out=None, out_dtype=None, flags: int = 0, 
     _check(lib().fp4q_decompress_mx(_ptr(codes), _ptr(scales), rows, L, _ptr(out),
                                     _out_dtype_code(out.dtype), flags, _stream(stream, gpu)))
     return out
+
+
+_LINEAR = ("FP4Q_GROUP8", "FP4Q_E4M3", "FP4Q_E5M2", "FP4Q_FLAG_TILES", "FP4Q_FLAG_ACCUMULATE", "RmsNorm",
+           "Quantized8", "fp4q_rmsnorm", "fp4q_rmsnorm_backward", "fp4q_quantize8", "fp4q_gemm8")
+
+
+def __getattr__(name):
+    """The 8-bit linear-layer operators, from their module at first use: it imports
+    torch, which the package itself leaves to the calls."""
+    if name in _LINEAR:
+        from . import linear
+        globals().update({n: getattr(linear, n) for n in _LINEAR})
+        return globals()[name]
+    raise AttributeError("module %r has no attribute %r" % (__name__, name))

@@ -1,0 +1,247 @@
+"""Binding of the library's 8-bit linear-layer operators (C ABI in
+``include/fp4q_linear.h``): root-mean-square norm with the residual's addition
+and 8-bit output, its gradients, quantisation to 8 bits with a scale per 128
+values, and the product of two 8-bit operands.
+
+As in the rest of the package the functions carry the C entry points' names and
+marshal arguments: torch tensors in, device pointers and the current HIP stream
+out.  8-bit codes are float8 tensors whose rows begin at multiples of 16 bytes
+(``stride(0) % 16 == 0``); scales are float32, [ceil(cols / 128), rows], or
+[ceil(cols / 128), ceil(rows / 128)] for 128 x 128 tiles.
+"""
+from __future__ import annotations
+
+import ctypes
+from typing import NamedTuple, Optional
+
+import torch
+
+from . import (FP4Q_ERR_SHAPE, FP4Q_OUT_BF16, FP4Q_OUT_F32, Fp4qError, _check, _dims, _empty, _on_gpu,
+               _stream)
+from . import lib as _base_lib
+
+FP4Q_GROUP8 = 128
+FP4Q_E4M3 = 0
+FP4Q_E5M2 = 1
+FP4Q_FLAG_TILES = 2
+FP4Q_FLAG_ACCUMULATE = 4
+
+_FORMATS = {torch.float8_e4m3fn: FP4Q_E4M3, torch.float8_e5m2: FP4Q_E5M2}
+_TYPES = {torch.float32: FP4Q_OUT_F32, torch.bfloat16: FP4Q_OUT_BF16}
+_bound = None
+
+
+def _lib() -> ctypes.CDLL:
+    global _bound
+    L = _base_lib()
+    if _bound is not L:
+        P, I, I64, U32, F = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_uint32, ctypes.c_float
+        Z, SZ = ctypes.c_size_t, ctypes.POINTER(ctypes.c_size_t)
+        L.fp4q_rmsnorm.argtypes = [P, P, P, F, I64, I64, I, P, P, P, I64, P, P, P]
+        L.fp4q_rmsnorm_backward_workspace.argtypes = [I64, I64, SZ]
+        L.fp4q_rmsnorm_backward.argtypes = [P, P, P, P, P, I64, I64, I, P, P, P, Z, P]
+        L.fp4q_quantize8.argtypes = [P, I64, I64, I, I, P, I64, P, P, I64, P, U32, P]
+        L.fp4q_gemm8_workspace.argtypes = [I64, I64, I64, U32, SZ]
+        L.fp4q_gemm8.argtypes = [P, I64, I, P, P, I64, I, P, I64, I64, I64, P, I, U32, P, Z, P]
+        _bound = L
+    return L
+
+
+def _groups(n: int) -> int:
+    return (n + FP4Q_GROUP8 - 1) // FP4Q_GROUP8
+
+
+def _like(t, name, shape, dtype):
+    """A tensor argument of exactly this shape and type, contiguous."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("fp4q: %s must be a torch tensor" % name)
+    if t.dtype != dtype:
+        raise TypeError("fp4q: %s must be %s, got %s" % (name, dtype, t.dtype))
+    if tuple(t.shape) != shape:
+        raise ValueError("fp4q: %s must have shape %s, has %s" % (name, shape, tuple(t.shape)))
+    if not t.is_contiguous():
+        raise ValueError("fp4q: %s must be contiguous" % name)
+    return t
+
+
+def _typed(t, name):
+    """The type code of a 2-D contiguous float32 or bfloat16 tensor, and its shape."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("fp4q: %s must be a torch tensor" % name)
+    code = _TYPES.get(t.dtype)
+    if code is None:
+        raise TypeError("fp4q: %s must be float32 or bfloat16, got %s" % (name, t.dtype))
+    rows, cols = _dims(t)
+    if cols == 0:
+        raise Fp4qError(FP4Q_ERR_SHAPE)
+    return code, rows, cols
+
+
+def _codes_out(rows, cols, dtype, device, stream):
+    """Uninitialised codes [rows, cols] whose rows begin at multiples of 16 bytes."""
+    pitch = (cols + 15) // 16 * 16
+    t = _empty((rows, pitch), dtype, device, stream)
+    return t if pitch == cols else t[:, :cols]
+
+
+def _codes_in(t, name):
+    """Format, rows, cols and pitch of an 8-bit operand; its rows must be readable up
+    to a multiple of 16 bytes (the kernels load 16 bytes at a time)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("fp4q: %s must be a torch tensor" % name)
+    fmt = _FORMATS.get(t.dtype)
+    if fmt is None:
+        raise TypeError("fp4q: %s must be float8_e4m3fn or float8_e5m2, got %s" % (name, t.dtype))
+    if t.dim() != 2:
+        raise ValueError("fp4q: expected a 2-D tensor [rows, cols]")
+    rows, cols = t.shape
+    wide = (cols + 15) // 16 * 16
+    pitch = t.stride(0) if rows > 1 else wide
+    if rows and cols:
+        if cols > 1 and t.stride(1) != 1:
+            raise ValueError("fp4q: the columns of %s must be contiguous" % name)
+        if pitch % 16 or pitch < cols:
+            raise ValueError("fp4q: the rows of %s must begin at multiples of 16 bytes" % name)
+        if t.storage_offset() + (rows - 1) * pitch + wide > t.untyped_storage().nbytes():
+            raise ValueError("fp4q: the last row of %s must be readable up to a multiple of 16 bytes" % name)
+    else:
+        pitch = wide
+    return fmt, rows, cols, pitch
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
+class RmsNorm(NamedTuple):
+    """What :func:`fp4q_rmsnorm` returns; what was not asked for is None."""
+    h: torch.Tensor
+    y: Optional[torch.Tensor]
+    codes: Optional[torch.Tensor]
+    scales: Optional[torch.Tensor]
+    rstd: Optional[torch.Tensor]
+
+
+def fp4q_rmsnorm(x, weight, eps: float, residual=None, h=None, want_y: bool = True,
+                 want_codes: bool = False, want_rstd: bool = False, stream=None) -> RmsNorm:
+    """h = x + residual (x itself without one), y = h / sqrt(mean(h^2) + eps) * weight of
+    a float32 or bfloat16 tensor [rows, cols]: y in that type (want_y) and/or as E4M3
+    codes [rows, cols] with scales [ceil(cols / 128), rows] (want_codes), and the
+    reciprocal roots (want_rstd) that the backward pass takes.  ``h=residual`` updates
+    the residual in place."""
+    dtype, rows, cols = _typed(x, "input")
+    _like(weight, "weight", (cols,), x.dtype)
+    ins = [x, weight]
+    if residual is not None:
+        ins.append(_like(residual, "residual", (rows, cols), x.dtype))
+        if h is not None:
+            ins.append(_like(h, "h", (rows, cols), x.dtype))
+        else:
+            h = _empty((rows, cols), x.dtype, x.device, stream)
+    elif h is not None:
+        raise ValueError("fp4q: h is an output of the sum with a residual")
+    if not (want_y or want_codes):
+        raise ValueError("fp4q: ask for y, codes or both")
+    gpu = _on_gpu(*ins)
+    y = _empty((rows, cols), x.dtype, gpu, stream) if want_y else None
+    codes = scales = None
+    if want_codes:
+        codes = _codes_out(rows, cols, torch.float8_e4m3fn, gpu, stream)
+        scales = _empty((_groups(cols), rows), torch.float32, gpu, stream)
+    rstd = _empty((rows,), torch.float32, gpu, stream) if want_rstd else None
+    _check(_lib().fp4q_rmsnorm(_at(x), _at(residual), _at(weight), eps, rows, cols, dtype, _at(h), _at(y),
+                               _at(codes), (cols + 15) // 16 * 16, _at(scales), _at(rstd),
+                               _stream(stream, gpu)))
+    return RmsNorm(x if residual is None else h, y, codes, scales, rstd)
+
+
+def fp4q_rmsnorm_backward(dy, h, weight, rstd, dh=None, stream=None):
+    """Gradients of :func:`fp4q_rmsnorm` -> (dx, dweight): dx is the gradient of x and of
+    the residual alike, in the inputs' type; dweight is float32 [cols].  ``h`` is the
+    forward's h, ``dh`` the gradient that reaches h by other paths."""
+    dtype, rows, cols = _typed(dy, "dy")
+    _like(h, "h", (rows, cols), dy.dtype)
+    _like(weight, "weight", (cols,), dy.dtype)
+    _like(rstd, "rstd", (rows,), torch.float32)
+    ins = [dy, h, weight, rstd]
+    if dh is not None:
+        ins.append(_like(dh, "dh", (rows, cols), dy.dtype))
+    gpu = _on_gpu(*ins)
+    need = ctypes.c_size_t()
+    _check(_lib().fp4q_rmsnorm_backward_workspace(rows, cols, ctypes.byref(need)))
+    dx = _empty((rows, cols), dy.dtype, gpu, stream)
+    dweight = _empty((cols,), torch.float32, gpu, stream)
+    space = _empty((need.value,), torch.uint8, gpu, stream)
+    _check(_lib().fp4q_rmsnorm_backward(_at(dy), _at(h), _at(weight), _at(rstd), _at(dh), rows, cols, dtype,
+                                        _at(dx), _at(dweight), _at(space), need.value, _stream(stream, gpu)))
+    return dx, dweight
+
+
+class Quantized8(NamedTuple):
+    """What :func:`fp4q_quantize8` returns; what was not asked for is None."""
+    codes: Optional[torch.Tensor]
+    scales: Optional[torch.Tensor]
+    codes_t: Optional[torch.Tensor]
+    scales_t: Optional[torch.Tensor]
+
+
+def fp4q_quantize8(x, dtype=torch.float8_e4m3fn, tiles: bool = False, straight: bool = True,
+                   transposed: bool = False, stream=None) -> Quantized8:
+    """8-bit codes and scales of a float32 or bfloat16 tensor [rows, cols]: of x
+    (straight) and/or of its transpose (transposed), with one scale per 128
+    neighbours of a row of what is written, or per 128 x 128 tile (tiles)."""
+    kind, rows, cols = _typed(x, "input")
+    fmt = _FORMATS.get(dtype)
+    if fmt is None:
+        raise TypeError("fp4q: codes are float8_e4m3fn or float8_e5m2, not %s" % (dtype,))
+    if not (straight or transposed):
+        raise ValueError("fp4q: ask for straight, transposed or both")
+    gpu = _on_gpu(x)
+    codes = scales = codes_t = scales_t = None
+    gr, gc = _groups(rows), _groups(cols)
+    if straight:
+        codes = _codes_out(rows, cols, dtype, gpu, stream)
+        scales = _empty((gc, gr if tiles else rows), torch.float32, gpu, stream)
+    if transposed:
+        codes_t = _codes_out(cols, rows, dtype, gpu, stream)
+        scales_t = _empty((gr, gc if tiles else cols), torch.float32, gpu, stream)
+    _check(_lib().fp4q_quantize8(_at(x), rows, cols, kind, fmt, _at(codes), (cols + 15) // 16 * 16, _at(scales),
+                                 _at(codes_t), (rows + 15) // 16 * 16, _at(scales_t),
+                                 FP4Q_FLAG_TILES if tiles else 0, _stream(stream, gpu)))
+    return Quantized8(codes, scales, codes_t, scales_t)
+
+
+def fp4q_gemm8(a, a_scales, b, b_scales, out=None, out_dtype=None, accumulate: bool = False, stream=None):
+    """The product of two 8-bit operands: a [M, K] with a_scales [ceil(K / 128), M] and
+    b [N, K] with b_scales [ceil(K / 128), N] or, for tiles, [ceil(K / 128), ceil(N / 128)]
+    -> [M, N] float32 or bfloat16 (bfloat16 when neither ``out`` nor ``out_dtype`` says
+    otherwise).  ``accumulate`` adds the product to a float32 ``out``."""
+    fa, M, K, a_pitch = _codes_in(a, "a")
+    fb, N, kb, b_pitch = _codes_in(b, "b")
+    if kb != K:
+        raise ValueError("fp4q: a has %d columns, b %d" % (K, kb))
+    groups = _groups(K)
+    _like(a_scales, "a's scales", (groups, M), torch.float32)
+    tiles = isinstance(b_scales, torch.Tensor) and tuple(b_scales.shape) == (groups, _groups(N))
+    _like(b_scales, "b's scales", (groups, _groups(N) if tiles else N), torch.float32)
+    ins = [a, a_scales, b, b_scales]
+    if out is not None:
+        if out_dtype is not None and out_dtype != out.dtype:
+            raise TypeError("fp4q: out is %s, out_dtype %s" % (out.dtype, out_dtype))
+        ins.append(_like(out, "out", (M, N), out.dtype))
+    elif accumulate:
+        raise ValueError("fp4q: accumulate needs out")
+    dtype = out.dtype if out is not None else out_dtype or torch.bfloat16
+    code = _TYPES.get(dtype)
+    if code is None or (accumulate and dtype != torch.float32):
+        raise TypeError("fp4q: out must be float32%s, got %s" % ("" if accumulate else " or bfloat16", dtype))
+    gpu = _on_gpu(*ins)
+    flags = (FP4Q_FLAG_TILES if tiles else 0) | (FP4Q_FLAG_ACCUMULATE if accumulate else 0)
+    need = ctypes.c_size_t()
+    _check(_lib().fp4q_gemm8_workspace(M, N, K, flags, ctypes.byref(need)))
+    if out is None:
+        out = _empty((M, N), dtype, gpu, stream)
+    space = _empty((need.value,), torch.uint8, gpu, stream) if need.value else None
+    _check(_lib().fp4q_gemm8(_at(a), a_pitch, fa, _at(a_scales), _at(b), b_pitch, fb, _at(b_scales), M, N, K,
+                             _at(out), code, flags, _at(space), need.value, _stream(stream, gpu)))
+    return out
