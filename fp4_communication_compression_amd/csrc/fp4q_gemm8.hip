@@ -81,9 +81,9 @@ struct Frag<kFmt, true> {
 // One block's product of a 16 x 16 tile.
 template <int kFirst, int kSecond>
 __device__ __forceinline__ f32x4 block_product(const Frag<kFirst, false> &first, const Frag<kSecond, false> &second) {
-    // scale operands 127 = 2^0: the matrix core's own scaling is not used
+    // with scale operands 0 this is the instruction without the matrix core's own scaling
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(first.v, second.v, f32x4{0, 0, 0, 0}, kFirst, kSecond,
-                                                            0, 127, 0, 127);
+                                                            0, 0, 0, 0);
 }
 template <int kFirst, int kSecond>
 __device__ __forceinline__ f32x4 block_product(const Frag<kFirst, true> &first, const Frag<kSecond, true> &second) {
@@ -93,118 +93,263 @@ __device__ __forceinline__ f32x4 block_product(const Frag<kFirst, true> &first, 
     return d;
 }
 
-// 16 bytes of a row at byte k of K: zero from K on.
-__device__ __forceinline__ u32x4 load_chunk(const uint8_t *row, int k, int K) {
-    if (k >= K) return u32x4{0, 0, 0, 0};
-    u32x4 w = *reinterpret_cast<const u32x4 *>(row + k);
-    const int left = K - k;
-    if (left < 16) {
+// A workgroup's tile: kWavesM x kWavesN wavefronts of kTilesM x kTilesN tiles of
+// 16 x 16 each, a block of 128 k at a time.
+template <int kWavesM_, int kWavesN_, int kTilesM_, int kTilesN_>
+struct Shape {
+    static constexpr int kWavesM = kWavesM_, kWavesN = kWavesN_, kTilesM = kTilesM_, kTilesN = kTilesN_;
+    static constexpr int kWaveM = 16 * kTilesM, kWaveN = 16 * kTilesN;
+    static constexpr int kM = kWavesM * kWaveM, kN = kWavesN * kWaveN;
+    static constexpr int kWaves = kWavesM * kWavesN;
+    static constexpr int kThreads = kWave * kWaves;
+    static constexpr int kLoads = (kM + kN) / 8 / kWaves;  // 8 rows of 128 bytes per load and wavefront
+    static_assert((kM + kN) % (8 * kWaves) == 0 && kM % 8 == 0, "whole loads");
+};
+
+typedef __attribute__((address_space(3))) void lds_void;
+
+// One block of both operands with its scales, as staged in LDS.  Rows are 128 bytes;
+// chunk c (16 bytes) of row r lies at chunk c ^ (r & 7), so that 8 rows' equal
+// chunks meet 8 different bank groups.
+template <typename S>
+struct alignas(16) Stage {
+    u32x4 a[S::kM * 8], b[S::kN * 8];
+    float sa[S::kM], sb[S::kN];
+};
+
+template <typename S, int kFmtA, int kFmtB, bool kTiles, bool kPrecise>
+struct Tile {
+    const GemmArgs &p;
+    int lane, wave, m0, n0, wm, wn, row16, quarter;
+    int offset[S::kLoads];  // of each load's bytes from its operand's tile
+    __amdgpu_buffer_rsrc_t ra, rb;
+    f32x4 acc[S::kTilesM][S::kTilesN];
+
+    __device__ __forceinline__ Tile(const GemmArgs &args, int tm, int tn) : p(args) {
+        lane = threadIdx.x & (kWave - 1);
+        wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+        m0 = tm * S::kM;
+        n0 = tn * S::kN;
+        wm = wave % S::kWavesM * S::kWaveM;
+        wn = wave / S::kWavesM * S::kWaveN;
+        row16 = lane & 15;
+        quarter = lane >> 4;
+        // rows past the end repeat the last one, and the descriptors end with the last
+        // row's last whole 16 bytes: no load leaves an operand
+        const int rows_a = min(S::kM, p.M - m0), rows_b = min(S::kN, p.N - n0);
+        const int wide = (p.K + 15) & ~15;
+        ra = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(p.a) + (int64_t)m0 * p.a_pitch, 0,
+                                               (rows_a - 1) * (int)p.a_pitch + wide, 0x00020000);
+        rb = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(p.b) + (int64_t)n0 * p.b_pitch, 0,
+                                               (rows_b - 1) * (int)p.b_pitch + wide, 0x00020000);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int keep = left - 4 * i;
-            w[i] = keep >= 4 ? w[i] : keep <= 0 ? 0u : w[i] & ((1u << (8 * keep)) - 1);
+        for (int i = 0; i < S::kLoads; ++i) {
+            const int r = (i * S::kWaves + wave) * 8 + (lane >> 3), chunk = (lane & 7) ^ (lane >> 3);
+            const bool of_a = (i * S::kWaves + wave) * 8 < S::kM;
+            offset[i] = 16 * chunk + (of_a ? min(r, rows_a - 1) * (int)p.a_pitch
+                                           : min(r - S::kM, rows_b - 1) * (int)p.b_pitch);
         }
+#pragma unroll
+        for (int i = 0; i < S::kTilesM; ++i)
+#pragma unroll
+            for (int j = 0; j < S::kTilesN; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
     }
-    return w;
-}
 
-constexpr int kBM = 128, kBN = 128, kThreads = 256;
-
-// kTiles: b's scales are tiles.  LDS rows are 128 bytes, chunk c of row r at
-// chunk c ^ (r & 7).
-template <int kFmtA, int kFmtB, bool kTiles, bool kPrecise>
-__global__ __launch_bounds__(kThreads) void gemm_kernel(GemmArgs p) {
-    __shared__ u32x4 lds_a[kBM * 8], lds_b[kBN * 8];
-    const int t = threadIdx.x, lane = t & 63, wave = t / 64;
-    const int tm = (int)(blockIdx.x % (unsigned)p.tiles_m), tn = (int)(blockIdx.x / (unsigned)p.tiles_m);
-    const int m0 = tm * kBM, n0 = tn * kBN;
-    const int wm = (wave & 1) * 64, wn = (wave >> 1) * 64;
-    const int row16 = lane & 15, quarter = lane >> 4;
-    const int blocks = (p.K + kGroup - 1) / kGroup;
-    const int sb_pitch = kTiles ? (p.N + kGroup - 1) / kGroup : p.N;
-
-    f32x4 acc[4][4];
+    // Queues block kb's loads, straight into LDS.
+    __device__ __forceinline__ void fetch(Stage<S> &to, int kb) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
-
-    for (int kb = 0; kb < blocks; ++kb) {
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < kBM * 8 / kThreads; ++i) {
-            const int q = i * kThreads + t, r = q >> 3, c = q & 7;
-            const int m = min(m0 + r, p.M - 1), n = min(n0 + r, p.N - 1);
-            lds_a[r * 8 + (c ^ (r & 7))] = load_chunk(p.a + m * p.a_pitch, kb * kGroup + 16 * c, p.K);
-            lds_b[r * 8 + (c ^ (r & 7))] = load_chunk(p.b + n * p.b_pitch, kb * kGroup + 16 * c, p.K);
+        for (int i = 0; i < S::kLoads; ++i) {
+            const int r0 = (i * S::kWaves + wave) * 8;
+            if (r0 < S::kM)
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void *)(to.a + r0 * 8), 16, offset[i],
+                                                         kb * kGroup, 0, 0);
+            else
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_void *)(to.b + (r0 - S::kM) * 8), 16, offset[i],
+                                                         kb * kGroup, 0, 0);
         }
-        __syncthreads();
-        Frag<kFmtB, kPrecise> fb[4];
-        f32x4 sb[4];
+        // scales, 64 to a wavefront; of b's tiles one for each 128 columns
+        constexpr int kScalesB = kTiles ? (S::kN + kGroup - 1) / kGroup : S::kN;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int r = wn + j * 16 + row16;
-            fb[j].set(lds_b[r * 8 + ((2 * quarter) ^ (r & 7))], lds_b[r * 8 + ((2 * quarter + 1) ^ (r & 7))]);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int n = min(n0 + wn + j * 16 + 4 * quarter + e, p.N - 1);
-                sb[j][e] = p.sb[(int64_t)kb * sb_pitch + (kTiles ? n / kGroup : n)];
+        for (int k = 0; k < S::kM; k += kWave)
+            if (wave == k / kWave % S::kWaves) {
+                const float *from = p.sa + (int64_t)kb * p.M + min(m0 + k + lane, p.M - 1);
+                __builtin_amdgcn_global_load_lds(const_cast<float *>(from), (lds_void *)(to.sa + k), 4, 0, 0);
             }
-        }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int r = wm + i * 16 + row16;
-            Frag<kFmtA, kPrecise> fa;
-            fa.set(lds_a[r * 8 + ((2 * quarter) ^ (r & 7))], lds_a[r * 8 + ((2 * quarter + 1) ^ (r & 7))]);
-            const float sa = p.sa[(int64_t)kb * p.M + min(m0 + r, p.M - 1)];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const f32x4 d = block_product(fb[j], fa);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) acc[i][j][e] = fmaf(d[e], sa * sb[j][e], acc[i][j][e]);
+        for (int k = 0; k < kScalesB; k += kWave)
+            if (wave == S::kWaves - 1 - k / kWave % S::kWaves) {
+                const int cols = kTiles ? (p.N + kGroup - 1) / kGroup : p.N, c0 = kTiles ? n0 / kGroup : n0;
+                const float *from = p.sb + (int64_t)kb * cols + min(c0 + k + lane, cols - 1);
+                __builtin_amdgcn_global_load_lds(const_cast<float *>(from), (lds_void *)(to.sb + k), 4, 0, 0);
             }
-        }
     }
+
+    // Clears the codes from K on in the last block.
+    __device__ __forceinline__ void clear_tail(Stage<S> &in) {
+        const int left = p.K % kGroup;
+        for (int r = threadIdx.x; r < S::kM + S::kN; r += S::kThreads) {
+            u32x4 *row = r < S::kM ? in.a + r * 8 : in.b + (r - S::kM) * 8;
+            for (int c = left / 16; c < 8; ++c) {
+                u32x4 w = row[c ^ (r & 7)];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int m = m0 + wm + i * 16 + row16;
-        if (m >= p.M) continue;
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int n = n0 + wn + j * 16 + 4 * quarter + e;
-                if (n >= p.N) continue;
-                const int64_t at = (int64_t)m * p.N + n;
-                if (p.out_f32) {
-                    float *o = static_cast<float *>(p.out) + at;
-                    *o = p.accumulate ? *o + acc[i][j][e] : acc[i][j][e];
-                } else {
-                    static_cast<bf16 *>(p.out)[at] = from_float<bf16>(acc[i][j][e]);
+                for (int i = 0; i < 4; ++i) {
+                    const int keep = left - 16 * c - 4 * i;
+                    w[i] = keep >= 4 ? w[i] : keep <= 0 ? 0u : w[i] & ((1u << (8 * keep)) - 1);
                 }
+                row[c ^ (r & 7)] = w;
             }
+        }
     }
+
+    // Rows row .. row + 15; row is a multiple of 8.
+    template <int kFmt>
+    __device__ __forceinline__ Frag<kFmt, kPrecise> frag(const u32x4 *rows, int row) {
+        const u32x4 *mine = rows + row16 * 8 + row * 8;
+        Frag<kFmt, kPrecise> f;
+        f.set(mine[(2 * quarter) ^ (row16 & 7)], mine[(2 * quarter + 1) ^ (row16 & 7)]);
+        return f;
+    }
+
+    // The products run kLag tiles ahead of their scaled addition, so that the vector
+    // unit adds one tile while the matrix core works on the next ones.
+    __device__ __forceinline__ void multiply(const Stage<S> &in) {
+        constexpr int kLag = 3, kCount = S::kTilesM * S::kTilesN;
+        Frag<kFmtB, kPrecise> fb[S::kTilesN];
+        f32x4 sb[S::kTilesN], d[kLag + 1];
+        float sa[2], sb_tile = 1.0f;
+#pragma unroll
+        for (int j = 0; j < S::kTilesN; ++j) fb[j] = frag<kFmtB>(in.b, wn + j * 16);
+        Frag<kFmtA, kPrecise> fa[2];
+        fa[0] = frag<kFmtA>(in.a, wm);
+        sa[0] = in.sa[wm + row16];
+        if constexpr (kTiles) {
+            static_assert(kGroup % S::kWaveN == 0, "one tile of b's scales per wavefront");
+            sb_tile = in.sb[wn / kGroup];
+            sa[0] *= sb_tile;
+        } else {
+#pragma unroll
+            for (int j = 0; j < S::kTilesN; ++j)
+                sb[j] = *reinterpret_cast<const f32x4 *>(in.sb + wn + j * 16 + 4 * quarter);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int t = 0; t < kCount + kLag; ++t) {
+            const int i = t / S::kTilesN, j = t % S::kTilesN;
+            if (t < kCount) {
+                if (j == 0 && i + 1 < S::kTilesM) fa[(i + 1) & 1] = frag<kFmtA>(in.a, wm + (i + 1) * 16);
+                if (j == S::kTilesN - 1 && i + 1 < S::kTilesM)
+                    sa[(i + 1) & 1] = in.sa[wm + (i + 1) * 16 + row16] * sb_tile;
+                d[t % (kLag + 1)] = block_product(fb[j], fa[i & 1]);
+            }
+            if (t >= kLag) {
+                const int ui = (t - kLag) / S::kTilesN, uj = (t - kLag) % S::kTilesN;
+                const f32x4 v = d[(t - kLag) % (kLag + 1)];
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    acc[ui][uj][e] = fmaf(v[e], kTiles ? sa[ui & 1] : sa[ui & 1] * sb[uj][e], acc[ui][uj][e]);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        // the sums are due here: without this the compiler moves the work above into the
+        // next block's branches and keeps all fragments alive for it
+#pragma unroll
+        for (int i = 0; i < S::kTilesM; ++i)
+#pragma unroll
+            for (int j = 0; j < S::kTilesN; ++j) asm volatile("" : "+v"(acc[i][j]));
+    }
+
+    __device__ __forceinline__ void store() {
+#pragma unroll
+        for (int i = 0; i < S::kTilesM; ++i) {
+            const int m = m0 + wm + i * 16 + row16;
+            if (m >= p.M) continue;
+#pragma unroll
+            for (int j = 0; j < S::kTilesN; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int n = n0 + wn + j * 16 + 4 * quarter + e;
+                    if (n >= p.N) continue;
+                    const int64_t at = (int64_t)m * p.N + n;
+                    if (kPrecise) {
+                        float *o = static_cast<float *>(p.out) + at;
+                        *o = p.accumulate ? *o + acc[i][j][e] : acc[i][j][e];
+                    } else {
+                        static_cast<bf16 *>(p.out)[at] = from_float<bf16>(acc[i][j][e]);
+                    }
+                }
+        }
+    }
+};
+
+// Two blocks in LDS: one is multiplied while the next one's loads are under way.
+template <typename S, int kFmtA, int kFmtB, bool kTiles, bool kPrecise>
+__global__ __launch_bounds__(S::kThreads, 2) void gemm_kernel(GemmArgs p) {
+    __shared__ Stage<S> even;
+    __shared__ Stage<S> odd;
+    // consecutive workgroups go to the 8 XCDs in turn: each XCD takes a run of tiles,
+    // and a run walks 8 tiles of m before it steps in n, so that the tiles that an XCD
+    // works on at one time share their operands in its L2
+    const int count = p.tiles_m * p.tiles_n, each = count / 8, more = count % 8;
+    const int xcd = (int)blockIdx.x % 8, turn = (int)blockIdx.x / 8;
+    const int at = xcd * each + min(xcd, more) + turn;
+    const int band = at / (8 * p.tiles_n), in_band = at - band * 8 * p.tiles_n;
+    const int high = min(8, p.tiles_m - band * 8);
+    const int tm = band * 8 + in_band % high, tn = in_band / high;
+    Tile<S, kFmtA, kFmtB, kTiles, kPrecise> t(p, tm, tn);
+    const int blocks = (p.K + kGroup - 1) / kGroup, ragged = p.K % kGroup;
+    int kb = 0;
+    if (blocks & 1) {  // then pairs of blocks are left
+        t.fetch(odd, 0);
+        __syncthreads();
+        if (blocks > 1) {
+            t.fetch(even, 1);
+        } else if (ragged) {
+            t.clear_tail(odd);
+            __syncthreads();
+        }
+        t.multiply(odd);
+        kb = 1;
+    } else if (blocks) {
+        t.fetch(even, 0);
+    }
+    for (; kb < blocks; kb += 2) {
+        // the loads of block kb have landed, and nobody reads the other buffer
+        __syncthreads();
+        t.fetch(odd, kb + 1);
+        t.multiply(even);
+        __syncthreads();
+        if (kb + 2 < blocks) {
+            t.fetch(even, kb + 2);
+        } else if (ragged) {
+            t.clear_tail(odd);
+            __syncthreads();
+        }
+        t.multiply(odd);
+    }
+    t.store();
 }
 
-template <int kFmtA, int kFmtB>
-const void *pick(bool tiles, bool precise) {
-    if (precise)
-        return tiles ? (const void *)&gemm_kernel<kFmtA, kFmtB, true, true>
-                     : (const void *)&gemm_kernel<kFmtA, kFmtB, false, true>;
-    return tiles ? (const void *)&gemm_kernel<kFmtA, kFmtB, true, false>
-                 : (const void *)&gemm_kernel<kFmtA, kFmtB, false, false>;
+using Large = Shape<2, 4, 8, 4>;
+using LargePrecise = Shape<2, 4, 4, 4>;
+using Small = Shape<2, 2, 4, 4>;
+
+template <typename S, bool kPrecise, int kFmtA, int kFmtB>
+const void *pick(bool tiles) {
+    return tiles ? (const void *)&gemm_kernel<S, kFmtA, kFmtB, true, kPrecise>
+                 : (const void *)&gemm_kernel<S, kFmtA, kFmtB, false, kPrecise>;
 }
-const void *pick(int fa, int fb, bool tiles, bool precise) {
+template <typename S, bool kPrecise>
+const void *pick(int fa, int fb, bool tiles) {
     if (fa == FP4Q_E4M3)
-        return fb == FP4Q_E4M3 ? pick<FP4Q_E4M3, FP4Q_E4M3>(tiles, precise)
-                               : pick<FP4Q_E4M3, FP4Q_E5M2>(tiles, precise);
-    return fb == FP4Q_E4M3 ? pick<FP4Q_E5M2, FP4Q_E4M3>(tiles, precise)
-                           : pick<FP4Q_E5M2, FP4Q_E5M2>(tiles, precise);
+        return fb == FP4Q_E4M3 ? pick<S, kPrecise, FP4Q_E4M3, FP4Q_E4M3>(tiles)
+                               : pick<S, kPrecise, FP4Q_E4M3, FP4Q_E5M2>(tiles);
+    return fb == FP4Q_E4M3 ? pick<S, kPrecise, FP4Q_E5M2, FP4Q_E4M3>(tiles)
+                           : pick<S, kPrecise, FP4Q_E5M2, FP4Q_E5M2>(tiles);
 }
 
 bool bad_gemm(int64_t M, int64_t N, int64_t K) {
     return M < 0 || N < 0 || K < 0 || M >= kDimLimit || N >= kDimLimit || K >= kDimLimit ||
-           ceil_div(M, kBM) * ceil_div(N, kBN) > (int64_t)0x7FFFFFFF;
+           ceil_div(M, Small::kM) * ceil_div(N, Small::kN) > (int64_t)0x7FFFFFFF;
 }
 
 }  // namespace
@@ -245,9 +390,18 @@ int fp4q_gemm8(const uint8_t *a, int64_t a_pitch, int a_format, const float *a_s
                          rng(b_scales, 4 * groups * (tiles ? ceil_div(N, kGroup) : N))};
     if (clash(outs, 2, ins, K > 0 ? 4 : 0)) return FP4Q_ERR_ARG;
     GemmArgs p = {a, b, a_scales, b_scales, out, a_pitch, b_pitch, (int)M, (int)N, (int)K,
-                  (int)ceil_div(M, kBM), (int)ceil_div(N, kBN), out_dtype == FP4Q_OUT_F32, add};
+                  0, 0, out_dtype == FP4Q_OUT_F32, add};
     void *args[] = {&p};
-    return launch(pick(a_format, b_format, tiles, p.out_f32), dim3((unsigned)(p.tiles_m * p.tiles_n)), kThreads, args, stream);
+    const bool precise = p.out_f32;
+    const int lm = precise ? LargePrecise::kM : Large::kM, ln = precise ? LargePrecise::kN : Large::kN;
+    const bool large = ceil_div(M, lm) * ceil_div(N, ln) >= 200;
+    p.tiles_m = (int)ceil_div(M, large ? lm : Small::kM);
+    p.tiles_n = (int)ceil_div(N, large ? ln : Small::kN);
+    const void *fn = large ? precise ? pick<LargePrecise, true>(a_format, b_format, tiles)
+                                     : pick<Large, false>(a_format, b_format, tiles)
+                   : precise ? pick<Small, true>(a_format, b_format, tiles)
+                             : pick<Small, false>(a_format, b_format, tiles);
+    return launch(fn, dim3((unsigned)(p.tiles_m * p.tiles_n)), large ? 512 : 256, args, stream);
 }
 
 }  // extern "C"
