@@ -18,6 +18,9 @@
 //   16-bit matrix core (fp32 output) the codes become bf16, which holds every
 //     E4M3 and E5M2 value, and four v_mfma_f32_16x16x32_bf16 add their exact
 //     products in fp32: half the rate, 1e-8 per block.
+#include <type_traits>
+#include <utility>
+
 #include "fp4q_f8.h"
 
 namespace {
@@ -28,6 +31,16 @@ typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+
+// Calls f(std::integral_constant<int, I>) for I = 0 .. N-1.
+template <typename F, int... I>
+__device__ __forceinline__ void static_for_impl(F &&f, std::integer_sequence<int, I...>) {
+    (f(std::integral_constant<int, I>{}), ...);
+}
+template <int N, typename F>
+__device__ __forceinline__ void static_for(F &&f) {
+    static_for_impl(f, std::make_integer_sequence<int, N>{});
+}
 
 struct GemmArgs {
     const uint8_t *a, *b;
@@ -102,27 +115,36 @@ struct Shape {
     static constexpr int kM = kWavesM * kWaveM, kN = kWavesN * kWaveN;
     static constexpr int kWaves = kWavesM * kWavesN;
     static constexpr int kThreads = kWave * kWaves;
-    static constexpr int kLoads = (kM + kN) / 8 / kWaves;  // 8 rows of 128 bytes per load and wavefront
-    static_assert((kM + kN) % (8 * kWaves) == 0 && kM % 8 == 0, "whole loads");
+    // loads of 8 rows of 128 bytes for a wavefront and block
+    static constexpr int kLoadsA = kM / 8 / kWaves, kLoadsB = kN / 8 / kWaves;
+    static_assert(kM % (8 * kWaves) == 0 && kN % (8 * kWaves) == 0, "whole loads");
 };
 
 typedef __attribute__((address_space(3))) void lds_void;
 
 // One block of both operands with its scales, as staged in LDS.  Rows are 128 bytes;
-// chunk c (16 bytes) of row r lies at chunk c ^ (r & 7), so that 8 rows' equal
-// chunks meet 8 different bank groups.
+// chunk c (16 bytes) of row r lies at chunk c ^ (r / 2 & 7), so that 16 rows' equal
+// chunks (which a 16-byte read takes at once) meet 16 different groups of banks.
 template <typename S>
 struct alignas(16) Stage {
     u32x4 a[S::kM * 8], b[S::kN * 8];
     float sa[S::kM], sb[S::kN];
 };
 
+// A meeting of the workgroup's wavefronts, each with its loads into LDS landed: the
+// barrier alone waits for a wavefront's LDS reads and writes, not for those loads.
+__device__ __forceinline__ void meet() {
+    __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0)
+    __syncthreads();
+}
+
 template <typename S, int kFmtA, int kFmtB, bool kTiles, bool kPrecise>
 struct Tile {
     const GemmArgs &p;
     int lane, wave, m0, n0, wm, wn, row16, quarter;
-    int offset[S::kLoads];  // of each load's bytes from its operand's tile
-    __amdgpu_buffer_rsrc_t ra, rb;
+    int offset_a, offset_b;  // of a lane's 16 bytes from the 8 rows that its wavefront loads at once
+    const uint8_t *from_a, *from_b;  // the tile's rows
+    int bytes_a, bytes_b;            // to the end of their last one's last whole 16 bytes
     f32x4 acc[S::kTilesM][S::kTilesN];
 
     __device__ __forceinline__ Tile(const GemmArgs &args, int tm, int tn) : p(args) {
@@ -134,54 +156,59 @@ struct Tile {
         wn = wave / S::kWavesM * S::kWaveN;
         row16 = lane & 15;
         quarter = lane >> 4;
-        // rows past the end repeat the last one, and the descriptors end with the last
-        // row's last whole 16 bytes: no load leaves an operand
-        const int rows_a = min(S::kM, p.M - m0), rows_b = min(S::kN, p.N - n0);
         const int wide = (p.K + 15) & ~15;
-        ra = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(p.a) + (int64_t)m0 * p.a_pitch, 0,
-                                               (rows_a - 1) * (int)p.a_pitch + wide, 0x00020000);
-        rb = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(p.b) + (int64_t)n0 * p.b_pitch, 0,
-                                               (rows_b - 1) * (int)p.b_pitch + wide, 0x00020000);
-#pragma unroll
-        for (int i = 0; i < S::kLoads; ++i) {
-            const int r = (i * S::kWaves + wave) * 8 + (lane >> 3), chunk = (lane & 7) ^ (lane >> 3);
-            const bool of_a = (i * S::kWaves + wave) * 8 < S::kM;
-            offset[i] = 16 * chunk + (of_a ? min(r, rows_a - 1) * (int)p.a_pitch
-                                           : min(r - S::kM, rows_b - 1) * (int)p.b_pitch);
-        }
+        from_a = p.a + (int64_t)m0 * p.a_pitch;
+        from_b = p.b + (int64_t)n0 * p.b_pitch;
+        bytes_a = (min(S::kM, p.M - m0) - 1) * (int)p.a_pitch + wide;
+        bytes_b = (min(S::kN, p.N - n0) - 1) * (int)p.b_pitch + wide;
+        static_assert(S::kWaves % 2 == 0, "the rows of a wavefront's loads have one swizzle");
+        const int chunk = (lane & 7) ^ ((wave * 8 + (lane >> 3)) >> 1 & 7);
+        offset_a = (lane >> 3) * (int)p.a_pitch + 16 * chunk;
+        offset_b = (lane >> 3) * (int)p.b_pitch + 16 * chunk;
 #pragma unroll
         for (int i = 0; i < S::kTilesM; ++i)
 #pragma unroll
             for (int j = 0; j < S::kTilesN; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
     }
 
-    // Queues block kb's loads, straight into LDS.
+    // Eight rows of one operand straight into LDS.  The descriptor begins with the first of
+    // them and ends with the operand, so rows past its end are not read (what their place
+    // in LDS holds only meets outputs that are not stored).
+    __device__ __forceinline__ void fetch_rows(u32x4 *to, const uint8_t *from, int bytes, int at, int offset) {
+        const __amdgpu_buffer_rsrc_t r =
+            __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(from) + at, 0, max(bytes - at, 0), 0x00020000);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void *)to, 16, offset, 0, 0, 0);
+    }
+
+    // Queues block kb's loads.
     __device__ __forceinline__ void fetch(Stage<S> &to, int kb) {
+        // (opaque, so that no product of the pitches stays in a register over the loop)
+        int a_pitch = (int)p.a_pitch, b_pitch = (int)p.b_pitch;
+        asm volatile("" : "+s"(a_pitch), "+s"(b_pitch));
 #pragma unroll
-        for (int i = 0; i < S::kLoads; ++i) {
-            const int r0 = (i * S::kWaves + wave) * 8;
-            if (r0 < S::kM)
-                __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void *)(to.a + r0 * 8), 16, offset[i],
-                                                         kb * kGroup, 0, 0);
-            else
-                __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_void *)(to.b + (r0 - S::kM) * 8), 16, offset[i],
-                                                         kb * kGroup, 0, 0);
+        for (int i = 0; i < S::kLoadsA; ++i) {
+            const int r = (i * S::kWaves + wave) * 8;
+            fetch_rows(to.a + r * 8, from_a, bytes_a, r * a_pitch + kb * kGroup, offset_a);
         }
-        // scales, 64 to a wavefront; of b's tiles one for each 128 columns
+#pragma unroll
+        for (int i = 0; i < S::kLoadsB; ++i) {
+            const int r = (i * S::kWaves + wave) * 8;
+            fetch_rows(to.b + r * 8, from_b, bytes_b, r * b_pitch + kb * kGroup, offset_b);
+        }
+        // 64 scales a wavefront; of b's tiles one for each 128 columns
         constexpr int kScalesB = kTiles ? (S::kN + kGroup - 1) / kGroup : S::kN;
 #pragma unroll
         for (int k = 0; k < S::kM; k += kWave)
-            if (wave == k / kWave % S::kWaves) {
-                const float *from = p.sa + (int64_t)kb * p.M + min(m0 + k + lane, p.M - 1);
-                __builtin_amdgcn_global_load_lds(const_cast<float *>(from), (lds_void *)(to.sa + k), 4, 0, 0);
-            }
+            if (wave == k / kWave % S::kWaves) fetch_scales(to.sa + k, p.sa, p.M, kb, m0 + k);
+        const int cols = kTiles ? (p.N + kGroup - 1) / kGroup : p.N, c0 = kTiles ? n0 / kGroup : n0;
 #pragma unroll
         for (int k = 0; k < kScalesB; k += kWave)
-            if (wave == S::kWaves - 1 - k / kWave % S::kWaves) {
-                const int cols = kTiles ? (p.N + kGroup - 1) / kGroup : p.N, c0 = kTiles ? n0 / kGroup : n0;
-                const float *from = p.sb + (int64_t)kb * cols + min(c0 + k + lane, cols - 1);
-                __builtin_amdgcn_global_load_lds(const_cast<float *>(from), (lds_void *)(to.sb + k), 4, 0, 0);
-            }
+            if (wave == S::kWaves - 1 - k / kWave % S::kWaves) fetch_scales(to.sb + k, p.sb, cols, kb, c0 + k);
+    }
+    __device__ __forceinline__ void fetch_scales(float *to, const float *from, int count, int kb, int at) {
+        const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
+            const_cast<float *>(from) + (int64_t)kb * count + at, 0, max(min(count - at, kWave), 0) * 4, 0x00020000);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void *)to, 4, 4 * lane, 0, 0, 0);
     }
 
     // Clears the codes from K on in the last block.
@@ -190,93 +217,176 @@ struct Tile {
         for (int r = threadIdx.x; r < S::kM + S::kN; r += S::kThreads) {
             u32x4 *row = r < S::kM ? in.a + r * 8 : in.b + (r - S::kM) * 8;
             for (int c = left / 16; c < 8; ++c) {
-                u32x4 w = row[c ^ (r & 7)];
+                u32x4 w = row[c ^ (r >> 1 & 7)];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int keep = left - 16 * c - 4 * i;
                     w[i] = keep >= 4 ? w[i] : keep <= 0 ? 0u : w[i] & ((1u << (8 * keep)) - 1);
                 }
-                row[c ^ (r & 7)] = w;
+                row[c ^ (r >> 1 & 7)] = w;
             }
         }
     }
 
-    // Rows row .. row + 15; row is a multiple of 8.
+    // Rows row .. row + 15; row is a multiple of 16.
     template <int kFmt>
     __device__ __forceinline__ Frag<kFmt, kPrecise> frag(const u32x4 *rows, int row) {
         const u32x4 *mine = rows + row16 * 8 + row * 8;
         Frag<kFmt, kPrecise> f;
-        f.set(mine[(2 * quarter) ^ (row16 & 7)], mine[(2 * quarter + 1) ^ (row16 & 7)]);
+        f.set(mine[(2 * quarter) ^ (row16 >> 1)], mine[(2 * quarter + 1) ^ (row16 >> 1)]);
         return f;
     }
 
-    // The products run kLag tiles ahead of their scaled addition, so that the vector
-    // unit adds one tile while the matrix core works on the next ones.
-    __device__ __forceinline__ void multiply(const Stage<S> &in) {
-        constexpr int kLag = 3, kCount = S::kTilesM * S::kTilesN;
-        Frag<kFmtB, kPrecise> fb[S::kTilesN];
-        f32x4 sb[S::kTilesN], d[kLag + 1];
-        float sa[2], sb_tile = 1.0f;
-#pragma unroll
-        for (int j = 0; j < S::kTilesN; ++j) fb[j] = frag<kFmtB>(in.b, wn + j * 16);
-        Frag<kFmtA, kPrecise> fa[2];
-        fa[0] = frag<kFmtA>(in.a, wm);
-        sa[0] = in.sa[wm + row16];
-        if constexpr (kTiles) {
-            static_assert(kGroup % S::kWaveN == 0, "one tile of b's scales per wavefront");
-            sb_tile = in.sb[wn / kGroup];
-            sa[0] *= sb_tile;
-        } else {
-#pragma unroll
-            for (int j = 0; j < S::kTilesN; ++j)
-                sb[j] = *reinterpret_cast<const f32x4 *>(in.sb + wn + j * 16 + 4 * quarter);
-        }
-        __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-        for (int t = 0; t < kCount + kLag; ++t) {
-            const int i = t / S::kTilesN, j = t % S::kTilesN;
-            if (t < kCount) {
-                if (j == 0 && i + 1 < S::kTilesM) fa[(i + 1) & 1] = frag<kFmtA>(in.a, wm + (i + 1) * 16);
-                if (j == S::kTilesN - 1 && i + 1 < S::kTilesM)
-                    sa[(i + 1) & 1] = in.sa[wm + (i + 1) * 16 + row16] * sb_tile;
-                d[t % (kLag + 1)] = block_product(fb[j], fa[i & 1]);
+    // What a block's multiplication begins with, read during the one before it.
+    struct Head {
+        Frag<kFmtB, kPrecise> b[S::kTilesN];
+        Frag<kFmtA, kPrecise> a;
+        float sa, sb;
+    };
+    __device__ __forceinline__ float scale_a(const Stage<S> &in, int i) { return in.sa[wm + i * 16 + row16]; }
+    __device__ __forceinline__ void read_head(const Stage<S> &in, Head &h, int item) {
+        if (item == 0) {
+            h.a = frag<kFmtA>(in.a, wm);
+            h.sa = scale_a(in, 0);
+            h.sb = 1.0f;
+            if constexpr (kTiles) {
+                static_assert(kGroup % S::kWaveN == 0, "one tile of b's scales per wavefront");
+                h.sb = in.sb[wn / kGroup];
             }
-            if (t >= kLag) {
-                const int ui = (t - kLag) / S::kTilesN, uj = (t - kLag) % S::kTilesN;
+        } else {
+            h.b[item - 1] = frag<kFmtB>(in.b, wn + (item - 1) * 16);
+        }
+    }
+
+    // b's tiles in a head; the other ones are read at the block's beginning
+    static constexpr int kHeadB = S::kTilesN - 2;
+    // rows of a's tiles multiplied before the wavefronts meet, and rows read by the end of row i
+    static constexpr int kMeet = S::kTilesM * 3 / 4;
+    static constexpr int rows_read(int i) { return i + 3 < S::kTilesM ? i + 3 : S::kTilesM; }
+    static_assert(rows_read(kMeet - 1) == S::kTilesM, "the block is in registers when the wavefronts meet");
+    // items of the next block's head read by the end of row i >= kMeet
+    static constexpr int head_read(int i) {
+        const int before = i > kMeet ? head_read(i - 1) : 0;
+        return before + (kHeadB + 1 - before) / (S::kTilesM - i);
+    }
+
+    // Multiplies the block in `cur`.  At three quarters, when all of it is in registers,
+    // the wavefronts meet: the next block's loads have landed in `nxt` then, and those of
+    // the one after it can go to `cur`.  The last quarter reads the next block's head, so
+    // no wavefront waits for LDS at a block's beginning.  The products run kLag tiles
+    // ahead of their scaled addition, so that the vector unit adds one tile while the
+    // matrix core works on the next ones.
+    __device__ __forceinline__ void step(Stage<S> &cur, Stage<S> &nxt, Head &h, Head &n, int kb, int blocks) {
+        constexpr int kLag = 2, kTilesM = S::kTilesM, kTilesN = S::kTilesN;
+        constexpr int kCount = kTilesM * kTilesN;
+        Frag<kFmtA, kPrecise> fa[kTilesM];
+        float sa[kTilesM];
+        f32x4 sb[kTilesN], d[kLag + 1];
+        fa[0] = h.a;
+        sa[0] = h.sa * h.sb;
+#pragma unroll
+        for (int j = kHeadB; j < kTilesN; ++j) h.b[j] = frag<kFmtB>(cur.b, wn + j * 16);
+        if constexpr (!kTiles) {
+#pragma unroll
+            for (int j = 0; j < kTilesN; ++j)
+                sb[j] = *reinterpret_cast<const f32x4 *>(cur.sb + wn + j * 16 + 4 * quarter);
+        }
+        static_for<kCount + kLag>([&](auto step_of) {
+            constexpr int t = step_of.value, i = t / kTilesN, j = t % kTilesN;
+            if constexpr (j == 0 && i < kMeet) {
+                constexpr int from = i ? rows_read(i - 1) : 1, count = rows_read(i) - from;
+                static_for<count>([&](auto k) {
+                    fa[from + k.value] = frag<kFmtA>(cur.a, wm + (from + k.value) * 16);
+                    sa[from + k.value] = scale_a(cur, from + k.value) * h.sb;
+                });
+            }
+            if constexpr (t == kMeet * kTilesN) {
+                static_for<kMeet * kTilesN>([&](auto x) { asm volatile("" : "+v"(acc[x.value / kTilesN][x.value % kTilesN])); });
+                meet();
+                if (kb + 2 < blocks) {
+                    fetch(cur, kb + 2);
+                } else if (kb + 2 == blocks && p.K % kGroup) {
+                    clear_tail(nxt);
+                    __syncthreads();
+                }
+            }
+            if constexpr (j == 0 && i >= kMeet && i < kTilesM) {
+                constexpr int from = i > kMeet ? head_read(i - 1) : 0, count = head_read(i) - from;
+                static_for<count>([&](auto k) { read_head(nxt, n, from + k.value); });
+            }
+            if constexpr (t < kCount) d[t % (kLag + 1)] = block_product(h.b[j], fa[i]);
+            if constexpr (t >= kLag) {
+                constexpr int ui = (t - kLag) / kTilesN, uj = (t - kLag) % kTilesN;
                 const f32x4 v = d[(t - kLag) % (kLag + 1)];
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    acc[ui][uj][e] = fmaf(v[e], kTiles ? sa[ui & 1] : sa[ui & 1] * sb[uj][e], acc[ui][uj][e]);
+                    acc[ui][uj][e] = fmaf(v[e], kTiles ? sa[ui] : sa[ui] * sb[uj][e], acc[ui][uj][e]);
             }
             __builtin_amdgcn_sched_barrier(0);
-        }
-        // the sums are due here: without this the compiler moves the work above into the
-        // next block's branches and keeps all fragments alive for it
+        });
+        // the sums are due here: without this the compiler moves the work above into later
+        // branches and keeps the fragments alive for it
 #pragma unroll
-        for (int i = 0; i < S::kTilesM; ++i)
+        for (int i = 0; i < kTilesM; ++i)
 #pragma unroll
-            for (int j = 0; j < S::kTilesN; ++j) asm volatile("" : "+v"(acc[i][j]));
+            for (int j = 0; j < kTilesN; ++j) asm volatile("" : "+v"(acc[i][j]));
     }
 
-    __device__ __forceinline__ void store() {
+    // The sums leave a tile row (16 m) at a time through a part of LDS of the wavefront's
+    // own, from four neighbours a lane to whole rows: 16 bytes a lane where the output's
+    // rows allow it, else one element a lane.  Nobody reads LDS after the last meeting.
+    __device__ __forceinline__ void store(Stage<S> &room) {
+        using Out = std::conditional_t<kPrecise, float, bf16>;
+        constexpr int kPer16 = 16 / (int)sizeof(Out), kCols = S::kWaveN;
+        constexpr int kPitch = kCols + kPer16;  // elements; the shift keeps rows off each other's banks
+        static_assert(S::kWaves * 16 * kPitch * sizeof(Out) <= sizeof(room.a) + sizeof(room.b), "fits the stage");
+        Out *mine = reinterpret_cast<Out *>(&room) + wave * 16 * kPitch;
+        const int n1 = n0 + wn;
+        const bool wide = p.N % kPer16 == 0;
 #pragma unroll
         for (int i = 0; i < S::kTilesM; ++i) {
-            const int m = m0 + wm + i * 16 + row16;
-            if (m >= p.M) continue;
+            const int m1 = m0 + wm + i * 16;
+            if (m1 >= p.M || n1 >= p.N) break;
 #pragma unroll
-            for (int j = 0; j < S::kTilesN; ++j)
+            for (int j = 0; j < S::kTilesN; ++j) {
+                Out *to = mine + row16 * kPitch + j * 16 + 4 * quarter;
+                if constexpr (kPrecise) {
+                    *reinterpret_cast<f32x4 *>(to) = acc[i][j];
+                } else {
+                    u32x2 w;
+                    w[0] = fp4q_num::bf16_rne_pair(acc[i][j][0], acc[i][j][1]);
+                    w[1] = fp4q_num::bf16_rne_pair(acc[i][j][2], acc[i][j][3]);
+                    *reinterpret_cast<u32x2 *>(to) = w;
+                }
+            }
+            if (wide) {
+                constexpr int kLanes = kCols / kPer16, kRows = kWave / kLanes;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int n = n0 + wn + j * 16 + 4 * quarter + e;
-                    if (n >= p.N) continue;
-                    const int64_t at = (int64_t)m * p.N + n;
-                    if (kPrecise) {
-                        float *o = static_cast<float *>(p.out) + at;
-                        *o = p.accumulate ? *o + acc[i][j][e] : acc[i][j][e];
-                    } else {
-                        static_cast<bf16 *>(p.out)[at] = from_float<bf16>(acc[i][j][e]);
+                for (int k = 0; k < 16 / kRows; ++k) {
+                    const int r = k * kRows + lane / kLanes, c = lane % kLanes * kPer16;
+                    if (m1 + r < p.M && n1 + c < p.N) {
+                        u32x4 w = *reinterpret_cast<const u32x4 *>(mine + r * kPitch + c);
+                        u32x4 *to = reinterpret_cast<u32x4 *>(static_cast<Out *>(p.out) + (int64_t)(m1 + r) * p.N + n1 + c);
+                        if (kPrecise && p.accumulate) {
+                            const u32x4 had = *to;
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                w[e] = __float_as_uint(__uint_as_float(had[e]) + __uint_as_float(w[e]));
+                        }
+                        *to = w;
                     }
                 }
+            } else {
+                static_assert(kCols == kWave, "a lane for each column");
+                for (int r = 0; r < 16 && m1 + r < p.M; ++r)
+                    if (n1 + lane < p.N) {
+                        Out *to = static_cast<Out *>(p.out) + (int64_t)(m1 + r) * p.N + n1 + lane;
+                        Out v = mine[r * kPitch + lane];
+                        if constexpr (kPrecise)
+                            if (p.accumulate) v = *to + v;
+                        *to = v;
+                    }
+            }
         }
     }
 };
@@ -294,39 +404,30 @@ __global__ __launch_bounds__(S::kThreads, 2) void gemm_kernel(GemmArgs p) {
     const int at = xcd * each + min(xcd, more) + turn;
     const int band = at / (8 * p.tiles_n), in_band = at - band * 8 * p.tiles_n;
     const int high = min(8, p.tiles_m - band * 8);
-    const int tm = band * 8 + in_band % high, tn = in_band / high;
+    // (the divisions leave uniform values in vector registers; descriptors need scalars)
+    const int tm = __builtin_amdgcn_readfirstlane(band * 8 + in_band % high);
+    const int tn = __builtin_amdgcn_readfirstlane(in_band / high);
     Tile<S, kFmtA, kFmtB, kTiles, kPrecise> t(p, tm, tn);
     const int blocks = (p.K + kGroup - 1) / kGroup, ragged = p.K % kGroup;
-    int kb = 0;
-    if (blocks & 1) {  // then pairs of blocks are left
-        t.fetch(odd, 0);
-        __syncthreads();
-        if (blocks > 1) {
-            t.fetch(even, 1);
-        } else if (ragged) {
-            t.clear_tail(odd);
-            __syncthreads();
-        }
-        t.multiply(odd);
-        kb = 1;
-    } else if (blocks) {
+    if (blocks) {
+        typename decltype(t)::Head h0, h1;
+        int kb = 0;
         t.fetch(even, 0);
-    }
-    for (; kb < blocks; kb += 2) {
-        // the loads of block kb have landed, and nobody reads the other buffer
-        __syncthreads();
-        t.fetch(odd, kb + 1);
-        t.multiply(even);
-        __syncthreads();
-        if (kb + 2 < blocks) {
-            t.fetch(even, kb + 2);
-        } else if (ragged) {
-            t.clear_tail(odd);
+        if (blocks > 1) t.fetch(odd, 1);
+        meet();
+        if (blocks == 1 && ragged) {
+            t.clear_tail(even);
             __syncthreads();
         }
-        t.multiply(odd);
+#pragma unroll
+        for (int i = 0; i <= t.kHeadB; ++i) t.read_head(even, h0, i);
+        for (; kb + 1 < blocks; kb += 2) {
+            t.step(even, odd, h0, h1, kb, blocks);
+            t.step(odd, even, h1, h0, kb + 1, blocks);
+        }
+        if (kb < blocks) t.step(even, odd, h0, h1, kb, blocks);
     }
-    t.store();
+    t.store(even);
 }
 
 using Large = Shape<2, 4, 8, 4>;
