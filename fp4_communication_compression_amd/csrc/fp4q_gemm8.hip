@@ -127,8 +127,8 @@ typedef __attribute__((address_space(3))) void lds_void;
 // chunks (which a 16-byte read takes at once) meet 16 different groups of banks.
 template <typename S>
 struct alignas(16) Stage {
+    float sa[S::kM], sb[S::kN];  // first: within reach of a read's 16-bit offset
     u32x4 a[S::kM * 8], b[S::kN * 8];
-    float sa[S::kM], sb[S::kN];
 };
 
 // A meeting of the workgroup's wavefronts, each with its loads into LDS landed: the
@@ -277,13 +277,13 @@ struct Tile {
     // ahead of their scaled addition, so that the vector unit adds one tile while the
     // matrix core works on the next ones.
     __device__ __forceinline__ void step(Stage<S> &cur, Stage<S> &nxt, Head &h, Head &n, int kb, int blocks) {
-        constexpr int kLag = 2, kTilesM = S::kTilesM, kTilesN = S::kTilesN;
+        constexpr int kLag = 3, kTilesM = S::kTilesM, kTilesN = S::kTilesN;
         constexpr int kCount = kTilesM * kTilesN;
         Frag<kFmtA, kPrecise> fa[kTilesM];
         float sa[kTilesM];
         f32x4 sb[kTilesN], d[kLag + 1];
         fa[0] = h.a;
-        sa[0] = h.sa * h.sb;
+        sa[0] = h.sa;
 #pragma unroll
         for (int j = kHeadB; j < kTilesN; ++j) h.b[j] = frag<kFmtB>(cur.b, wn + j * 16);
         if constexpr (!kTiles) {
@@ -297,7 +297,7 @@ struct Tile {
                 constexpr int from = i ? rows_read(i - 1) : 1, count = rows_read(i) - from;
                 static_for<count>([&](auto k) {
                     fa[from + k.value] = frag<kFmtA>(cur.a, wm + (from + k.value) * 16);
-                    sa[from + k.value] = scale_a(cur, from + k.value) * h.sb;
+                    sa[from + k.value] = scale_a(cur, from + k.value);
                 });
             }
             if constexpr (t == kMeet * kTilesN) {
@@ -315,8 +315,10 @@ struct Tile {
                 static_for<count>([&](auto k) { read_head(nxt, n, from + k.value); });
             }
             if constexpr (t < kCount) d[t % (kLag + 1)] = block_product(h.b[j], fa[i]);
+            __builtin_amdgcn_sched_barrier(0);  // the matrix core first
             if constexpr (t >= kLag) {
                 constexpr int ui = (t - kLag) / kTilesN, uj = (t - kLag) % kTilesN;
+                if constexpr (kTiles && uj == 0) sa[ui] *= h.sb;
                 const f32x4 v = d[(t - kLag) % (kLag + 1)];
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
@@ -340,7 +342,7 @@ struct Tile {
         constexpr int kPer16 = 16 / (int)sizeof(Out), kCols = S::kWaveN;
         constexpr int kPitch = kCols + kPer16;  // elements; the shift keeps rows off each other's banks
         static_assert(S::kWaves * 16 * kPitch * sizeof(Out) <= sizeof(room.a) + sizeof(room.b), "fits the stage");
-        Out *mine = reinterpret_cast<Out *>(&room) + wave * 16 * kPitch;
+        Out *mine = reinterpret_cast<Out *>(room.a) + wave * 16 * kPitch;
         const int n1 = n0 + wn;
         const bool wide = p.N % kPer16 == 0;
 #pragma unroll
