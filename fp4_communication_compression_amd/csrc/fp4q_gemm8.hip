@@ -432,14 +432,153 @@ __global__ __launch_bounds__(S::kThreads, 2) void gemm_kernel(GemmArgs p) {
     t.store(even);
 }
 
+// 16 bytes of a row at byte k of K: zero from K on.
+__device__ __forceinline__ u32x4 load_chunk(const uint8_t *row, int k, int K) {
+    if (k >= K) return u32x4{0, 0, 0, 0};
+    u32x4 w = *reinterpret_cast<const u32x4 *>(row + k);
+    const int left = K - k;
+    if (left < 16) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int keep = left - 4 * i;
+            w[i] = keep >= 4 ? w[i] : keep <= 0 ? 0u : w[i] & ((1u << (8 * keep)) - 1);
+        }
+    }
+    return w;
+}
+
+// Few rows of a: the time is that of reading b once.  A workgroup takes 16 kNT rows of
+// b; its wavefronts share K, each taking every kWaves-th block, whole fragments straight
+// from memory into registers, kAhead blocks' loads at a time.  The parts of the sum are
+// joined through LDS in the wavefronts' order.
+template <int kMT_, int kNT_, int kWaves_, int kAhead_>
+struct Strip {
+    static constexpr int kMT = kMT_, kNT = kNT_, kWaves = kWaves_, kAhead = kAhead_;
+    static constexpr int kThreads = kWaves * kWave, kM = 16 * kMT, kN = 16 * kNT;
+};
+template <typename S, int kFmtA, int kFmtB, bool kTiles, bool kPrecise>
+__global__ __launch_bounds__(S::kThreads) void strip_kernel(GemmArgs p) {
+    __shared__ f32x4 part[S::kWaves][S::kMT * S::kNT][kWave];
+    const int lane = threadIdx.x & (kWave - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int row16 = lane & 15, quarter = lane >> 4;
+    const int n0 = (int)blockIdx.x * S::kN;
+    const int blocks = (p.K + kGroup - 1) / kGroup;
+    const int cols_sb = kTiles ? (p.N + kGroup - 1) / kGroup : p.N;
+    const uint8_t *a[S::kMT], *b[S::kNT];
+    int m[S::kMT];
+#pragma unroll
+    for (int i = 0; i < S::kMT; ++i) {
+        m[i] = min(i * 16 + row16, p.M - 1);
+        a[i] = p.a + m[i] * p.a_pitch;
+    }
+#pragma unroll
+    for (int j = 0; j < S::kNT; ++j) b[j] = p.b + min(n0 + j * 16 + row16, p.N - 1) * p.b_pitch;
+    f32x4 acc[S::kMT][S::kNT];
+#pragma unroll
+    for (int i = 0; i < S::kMT; ++i)
+#pragma unroll
+        for (int j = 0; j < S::kNT; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+
+    auto run = [&](int kb0, auto count_of, auto whole_of) {
+        constexpr int kCount = count_of.value;
+        constexpr bool kWhole = whole_of.value;  // no end of K inside
+        u32x4 fa[kCount][S::kMT][2], fb[kCount][S::kNT][2];
+        float sa[kCount][S::kMT];
+        f32x4 sb[kCount][S::kNT];
+#pragma unroll
+        for (int u = 0; u < kCount; ++u) {
+            const int kb = kb0 + u * S::kWaves, k = kb * kGroup + 32 * quarter;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                for (int j = 0; j < S::kNT; ++j)
+                    fb[u][j][h] = kWhole ? *reinterpret_cast<const u32x4 *>(b[j] + k + 16 * h)
+                                         : load_chunk(b[j], k + 16 * h, p.K);
+#pragma unroll
+                for (int i = 0; i < S::kMT; ++i)
+                    fa[u][i][h] = kWhole ? *reinterpret_cast<const u32x4 *>(a[i] + k + 16 * h)
+                                         : load_chunk(a[i], k + 16 * h, p.K);
+            }
+#pragma unroll
+            for (int i = 0; i < S::kMT; ++i) sa[u][i] = p.sa[(int64_t)kb * p.M + m[i]];
+#pragma unroll
+            for (int j = 0; j < S::kNT; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int n = min(n0 + j * 16 + 4 * quarter + e, p.N - 1);
+                    sb[u][j][e] = kTiles ? p.sb[(int64_t)kb * cols_sb + n0 / kGroup] : p.sb[(int64_t)kb * cols_sb + n];
+                }
+        }
+#pragma unroll
+        for (int u = 0; u < kCount; ++u)
+#pragma unroll
+            for (int j = 0; j < S::kNT; ++j) {
+                Frag<kFmtB, kPrecise> first;
+                first.set(fb[u][j][0], fb[u][j][1]);
+#pragma unroll
+                for (int i = 0; i < S::kMT; ++i) {
+                    Frag<kFmtA, kPrecise> second;
+                    second.set(fa[u][i][0], fa[u][i][1]);
+                    const f32x4 d = block_product(first, second);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[i][j][e] = fmaf(d[e], sa[u][i] * sb[u][j][e], acc[i][j][e]);
+                }
+            }
+    };
+    static_assert(kGroup % S::kN == 0, "one tile of b's scales per workgroup");
+    const int whole = p.K / kGroup;
+    int kb = wave;
+    for (; kb + (S::kAhead - 1) * S::kWaves < whole; kb += S::kAhead * S::kWaves)
+        run(kb, std::integral_constant<int, S::kAhead>{}, std::true_type{});
+    for (; kb < whole; kb += S::kWaves) run(kb, std::integral_constant<int, 1>{}, std::true_type{});
+    for (; kb < blocks; kb += S::kWaves) run(kb, std::integral_constant<int, 1>{}, std::false_type{});
+
+#pragma unroll
+    for (int i = 0; i < S::kMT; ++i)
+#pragma unroll
+        for (int j = 0; j < S::kNT; ++j) part[wave][i * S::kNT + j][lane] = acc[i][j];
+    __syncthreads();
+    for (int t = wave; t < S::kMT * S::kNT; t += S::kWaves) {
+        f32x4 sum = part[0][t][lane];
+#pragma unroll
+        for (int w = 1; w < S::kWaves; ++w) sum += part[w][t][lane];
+        const int row = t / S::kNT * 16 + row16, n = n0 + t % S::kNT * 16 + 4 * quarter;
+        if (row < p.M)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (n + e < p.N) {
+                    const int64_t at = (int64_t)row * p.N + n + e;
+                    if (kPrecise) {
+                        float *o = static_cast<float *>(p.out) + at;
+                        *o = p.accumulate ? *o + sum[e] : sum[e];
+                    } else {
+                        static_cast<bf16 *>(p.out)[at] = from_float<bf16>(sum[e]);
+                    }
+                }
+    }
+}
+
 using Large = Shape<2, 4, 8, 4>;
 using LargePrecise = Shape<2, 4, 4, 4>;
+using Strip16 = Strip<1, 1, 16, 4>;
+using Strip32 = Strip<2, 2, 8, 2>;
+using Strip64 = Strip<4, 2, 8, 2>;
 using Small = Shape<2, 2, 4, 4>;
 
+template <typename S, int kFmtA, int kFmtB, bool kTiles, bool kPrecise>
+struct Kernel {
+    static const void *get() { return (const void *)&gemm_kernel<S, kFmtA, kFmtB, kTiles, kPrecise>; }
+};
+template <int kMT, int kNT, int kWaves, int kAhead, int kFmtA, int kFmtB, bool kTiles, bool kPrecise>
+struct Kernel<Strip<kMT, kNT, kWaves, kAhead>, kFmtA, kFmtB, kTiles, kPrecise> {
+    static const void *get() {
+        return (const void *)&strip_kernel<Strip<kMT, kNT, kWaves, kAhead>, kFmtA, kFmtB, kTiles, kPrecise>;
+    }
+};
 template <typename S, bool kPrecise, int kFmtA, int kFmtB>
 const void *pick(bool tiles) {
-    return tiles ? (const void *)&gemm_kernel<S, kFmtA, kFmtB, true, kPrecise>
-                 : (const void *)&gemm_kernel<S, kFmtA, kFmtB, false, kPrecise>;
+    return tiles ? Kernel<S, kFmtA, kFmtB, true, kPrecise>::get() : Kernel<S, kFmtA, kFmtB, false, kPrecise>::get();
 }
 template <typename S, bool kPrecise>
 const void *pick(int fa, int fb, bool tiles) {
@@ -496,6 +635,14 @@ int fp4q_gemm8(const uint8_t *a, int64_t a_pitch, int a_format, const float *a_s
                   0, 0, out_dtype == FP4Q_OUT_F32, add};
     void *args[] = {&p};
     const bool precise = p.out_f32;
+    if (M <= 64) {
+        auto strip = [&](auto shape) {
+            using S = decltype(shape);
+            return launch(precise ? pick<S, true>(a_format, b_format, tiles) : pick<S, false>(a_format, b_format, tiles),
+                          dim3((unsigned)ceil_div(N, S::kN)), S::kThreads, args, stream);
+        };
+        return M <= 16 ? strip(Strip16{}) : M <= 32 ? strip(Strip32{}) : strip(Strip64{});
+    }
     const int lm = precise ? LargePrecise::kM : Large::kM, ln = precise ? LargePrecise::kN : Large::kN;
     const bool large = ceil_div(M, lm) * ceil_div(N, ln) >= 200;
     p.tiles_m = (int)ceil_div(M, large ? lm : Small::kM);

@@ -12,12 +12,12 @@ out.  8-bit codes are float8 tensors whose rows begin at multiples of 16 bytes
 from __future__ import annotations
 
 import ctypes
+import functools
 from typing import NamedTuple, Optional
 
 import torch
 
-from . import (FP4Q_ERR_SHAPE, FP4Q_OUT_BF16, FP4Q_OUT_F32, Fp4qError, _check, _dims, _empty, _on_gpu,
-               _stream)
+from . import FP4Q_ERR_SHAPE, FP4Q_OUT_BF16, FP4Q_OUT_F32, Fp4qError, _check, _empty, _stream
 from . import lib as _base_lib
 
 FP4Q_GROUP8 = 128
@@ -47,6 +47,35 @@ def _lib() -> ctypes.CDLL:
     return L
 
 
+# The checks and launches below run once per call of a serving step's smallest
+# operators, whose kernels take a few microseconds: they are written to cost little.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _launch_stream(stream, device):
+    """The address of the HIP stream to launch on (see _stream)."""
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(device.index)
+    return _stream(stream, device)
+
+
+def _gpu(*tensors):
+    """The one GPU that every tensor argument (None apart) lies on."""
+    first = tensors[0].get_device()
+    for t in tensors:
+        if t is not None and (t.get_device() != first or first < 0):
+            raise ValueError("fp4q: every tensor must be on the same GPU (%s, %s)" % (tensors[0].device, t.device))
+    return tensors[0].device
+
+
+@functools.lru_cache(maxsize=4096)
+def _workspace(which, *sizes) -> int:
+    """The workspace bytes that the C library asks for (a function of the sizes)."""
+    need = ctypes.c_size_t()
+    _check(getattr(_lib(), which)(*sizes, ctypes.byref(need)))
+    return need.value
+
+
 def _groups(n: int) -> int:
     return (n + FP4Q_GROUP8 - 1) // FP4Q_GROUP8
 
@@ -55,10 +84,10 @@ def _like(t, name, shape, dtype):
     """A tensor argument of exactly this shape and type, contiguous."""
     if not isinstance(t, torch.Tensor):
         raise TypeError("fp4q: %s must be a torch tensor" % name)
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError("fp4q: %s must be %s, got %s" % (name, dtype, t.dtype))
-    if tuple(t.shape) != shape:
-        raise ValueError("fp4q: %s must have shape %s, has %s" % (name, shape, tuple(t.shape)))
+    if t.shape != shape:
+        raise ValueError("fp4q: %s must have shape %s, has %s" % (name, tuple(shape), tuple(t.shape)))
     if not t.is_contiguous():
         raise ValueError("fp4q: %s must be contiguous" % name)
     return t
@@ -71,7 +100,11 @@ def _typed(t, name):
     code = _TYPES.get(t.dtype)
     if code is None:
         raise TypeError("fp4q: %s must be float32 or bfloat16, got %s" % (name, t.dtype))
-    rows, cols = _dims(t)
+    if t.dim() != 2:
+        raise ValueError("fp4q: expected a 2-D tensor [rows, cols]")
+    if not t.is_contiguous():
+        raise ValueError("fp4q: expected a contiguous tensor")
+    rows, cols = t.shape
     if cols == 0:
         raise Fp4qError(FP4Q_ERR_SHAPE)
     return code, rows, cols
@@ -130,20 +163,21 @@ def fp4q_rmsnorm(x, weight, eps: float, residual=None, h=None, want_y: bool = Tr
     reciprocal roots (want_rstd) that the backward pass takes.  ``h=residual`` updates
     the residual in place."""
     dtype, rows, cols = _typed(x, "input")
-    _like(weight, "weight", (cols,), x.dtype)
-    ins = [x, weight]
+    kind = x.dtype
+    _like(weight, "weight", (cols,), kind)
+    given = h
     if residual is not None:
-        ins.append(_like(residual, "residual", (rows, cols), x.dtype))
+        _like(residual, "residual", x.shape, kind)
         if h is not None:
-            ins.append(_like(h, "h", (rows, cols), x.dtype))
-        else:
-            h = _empty((rows, cols), x.dtype, x.device, stream)
+            _like(h, "h", x.shape, kind)
     elif h is not None:
         raise ValueError("fp4q: h is an output of the sum with a residual")
     if not (want_y or want_codes):
         raise ValueError("fp4q: ask for y, codes or both")
-    gpu = _on_gpu(*ins)
-    y = _empty((rows, cols), x.dtype, gpu, stream) if want_y else None
+    gpu = _gpu(x, weight, residual, given)
+    if residual is not None and h is None:
+        h = _empty((rows, cols), kind, gpu, stream)
+    y = _empty((rows, cols), kind, gpu, stream) if want_y else None
     codes = scales = None
     if want_codes:
         codes = _codes_out(rows, cols, torch.float8_e4m3fn, gpu, stream)
@@ -151,7 +185,7 @@ def fp4q_rmsnorm(x, weight, eps: float, residual=None, h=None, want_y: bool = Tr
     rstd = _empty((rows,), torch.float32, gpu, stream) if want_rstd else None
     _check(_lib().fp4q_rmsnorm(_at(x), _at(residual), _at(weight), eps, rows, cols, dtype, _at(h), _at(y),
                                _at(codes), (cols + 15) // 16 * 16, _at(scales), _at(rstd),
-                               _stream(stream, gpu)))
+                               _launch_stream(stream, gpu)))
     return RmsNorm(x if residual is None else h, y, codes, scales, rstd)
 
 
@@ -160,20 +194,18 @@ def fp4q_rmsnorm_backward(dy, h, weight, rstd, dh=None, stream=None):
     the residual alike, in the inputs' type; dweight is float32 [cols].  ``h`` is the
     forward's h, ``dh`` the gradient that reaches h by other paths."""
     dtype, rows, cols = _typed(dy, "dy")
-    _like(h, "h", (rows, cols), dy.dtype)
+    _like(h, "h", dy.shape, dy.dtype)
     _like(weight, "weight", (cols,), dy.dtype)
     _like(rstd, "rstd", (rows,), torch.float32)
-    ins = [dy, h, weight, rstd]
     if dh is not None:
-        ins.append(_like(dh, "dh", (rows, cols), dy.dtype))
-    gpu = _on_gpu(*ins)
-    need = ctypes.c_size_t()
-    _check(_lib().fp4q_rmsnorm_backward_workspace(rows, cols, ctypes.byref(need)))
+        _like(dh, "dh", dy.shape, dy.dtype)
+    gpu = _gpu(dy, h, weight, rstd, dh)
+    need = _workspace("fp4q_rmsnorm_backward_workspace", rows, cols)
     dx = _empty((rows, cols), dy.dtype, gpu, stream)
     dweight = _empty((cols,), torch.float32, gpu, stream)
-    space = _empty((need.value,), torch.uint8, gpu, stream)
+    space = _empty((need,), torch.uint8, gpu, stream)
     _check(_lib().fp4q_rmsnorm_backward(_at(dy), _at(h), _at(weight), _at(rstd), _at(dh), rows, cols, dtype,
-                                        _at(dx), _at(dweight), _at(space), need.value, _stream(stream, gpu)))
+                                        _at(dx), _at(dweight), _at(space), need, _launch_stream(stream, gpu)))
     return dx, dweight
 
 
@@ -196,7 +228,7 @@ def fp4q_quantize8(x, dtype=torch.float8_e4m3fn, tiles: bool = False, straight: 
         raise TypeError("fp4q: codes are float8_e4m3fn or float8_e5m2, not %s" % (dtype,))
     if not (straight or transposed):
         raise ValueError("fp4q: ask for straight, transposed or both")
-    gpu = _on_gpu(x)
+    gpu = _gpu(x)
     codes = scales = codes_t = scales_t = None
     gr, gc = _groups(rows), _groups(cols)
     if straight:
@@ -207,7 +239,7 @@ def fp4q_quantize8(x, dtype=torch.float8_e4m3fn, tiles: bool = False, straight: 
         scales_t = _empty((gr, gc if tiles else cols), torch.float32, gpu, stream)
     _check(_lib().fp4q_quantize8(_at(x), rows, cols, kind, fmt, _at(codes), (cols + 15) // 16 * 16, _at(scales),
                                  _at(codes_t), (rows + 15) // 16 * 16, _at(scales_t),
-                                 FP4Q_FLAG_TILES if tiles else 0, _stream(stream, gpu)))
+                                 FP4Q_FLAG_TILES if tiles else 0, _launch_stream(stream, gpu)))
     return Quantized8(codes, scales, codes_t, scales_t)
 
 
@@ -220,28 +252,27 @@ def fp4q_gemm8(a, a_scales, b, b_scales, out=None, out_dtype=None, accumulate: b
     fb, N, kb, b_pitch = _codes_in(b, "b")
     if kb != K:
         raise ValueError("fp4q: a has %d columns, b %d" % (K, kb))
-    groups = _groups(K)
+    groups, row_tiles = _groups(K), _groups(N)
     _like(a_scales, "a's scales", (groups, M), torch.float32)
-    tiles = isinstance(b_scales, torch.Tensor) and tuple(b_scales.shape) == (groups, _groups(N))
-    _like(b_scales, "b's scales", (groups, _groups(N) if tiles else N), torch.float32)
-    ins = [a, a_scales, b, b_scales]
+    tiles = isinstance(b_scales, torch.Tensor) and b_scales.shape == (groups, row_tiles)
+    _like(b_scales, "b's scales", (groups, row_tiles if tiles else N), torch.float32)
+    dtype = out_dtype or torch.bfloat16
     if out is not None:
         if out_dtype is not None and out_dtype != out.dtype:
             raise TypeError("fp4q: out is %s, out_dtype %s" % (out.dtype, out_dtype))
-        ins.append(_like(out, "out", (M, N), out.dtype))
+        dtype = out.dtype
+        _like(out, "out", (M, N), dtype)
     elif accumulate:
         raise ValueError("fp4q: accumulate needs out")
-    dtype = out.dtype if out is not None else out_dtype or torch.bfloat16
     code = _TYPES.get(dtype)
-    if code is None or (accumulate and dtype != torch.float32):
+    if code is None or (accumulate and code != FP4Q_OUT_F32):
         raise TypeError("fp4q: out must be float32%s, got %s" % ("" if accumulate else " or bfloat16", dtype))
-    gpu = _on_gpu(*ins)
+    gpu = _gpu(a, a_scales, b, b_scales, out)
     flags = (FP4Q_FLAG_TILES if tiles else 0) | (FP4Q_FLAG_ACCUMULATE if accumulate else 0)
-    need = ctypes.c_size_t()
-    _check(_lib().fp4q_gemm8_workspace(M, N, K, flags, ctypes.byref(need)))
+    need = _workspace("fp4q_gemm8_workspace", M, N, K, flags)
     if out is None:
         out = _empty((M, N), dtype, gpu, stream)
-    space = _empty((need.value,), torch.uint8, gpu, stream) if need.value else None
+    space = _empty((need,), torch.uint8, gpu, stream) if need else None
     _check(_lib().fp4q_gemm8(_at(a), a_pitch, fa, _at(a_scales), _at(b), b_pitch, fb, _at(b_scales), M, N, K,
-                             _at(out), code, flags, _at(space), need.value, _stream(stream, gpu)))
+                             _at(out), code, flags, _at(space), need, _launch_stream(stream, gpu)))
     return out
