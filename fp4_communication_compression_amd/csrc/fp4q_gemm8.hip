@@ -32,6 +32,7 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
+#define FP4Q_INLINE __attribute__((always_inline))
 // Calls f(std::integral_constant<int, I>) for I = 0 .. N-1.
 template <typename F, int... I>
 __device__ __forceinline__ void static_for_impl(F &&f, std::integer_sequence<int, I...>) {
@@ -50,6 +51,11 @@ struct GemmArgs {
     int M, N, K;
     int tiles_m, tiles_n;
     int out_f32, accumulate;
+    // K in `parts` runs of blocks, a workgroup each; with more than one, run s's sums go
+    // to partial + s part_size, and join_kernel adds them
+    int parts;
+    int64_t part_size;
+    float *partial;
 };
 
 // 32 codes of one row (half a block's 64 for every 16 lanes, in the order that both
@@ -127,14 +133,38 @@ typedef __attribute__((address_space(3))) void lds_void;
 // chunks (which a 16-byte read takes at once) meet 16 different groups of banks.
 template <typename S>
 struct alignas(16) Stage {
-    float sa[S::kM], sb[S::kN];  // first: within reach of a read's 16-bit offset
+    static constexpr int kScalesA = (S::kM + kWave - 1) / kWave * kWave;
+    float scales[kScalesA + S::kN];  // a's, then b's; first: within reach of a read's 16-bit offset
     u32x4 a[S::kM * 8], b[S::kN * 8];
 };
 
-// A meeting of the workgroup's wavefronts, each with its loads into LDS landed: the
-// barrier alone waits for a wavefront's LDS reads and writes, not for those loads.
+// kBytes (4 or 16) a lane from `bytes` bytes at `from` straight into LDS at `to` (uniform;
+// lane l's part goes to to + kBytes l).  Lanes whose offset lies outside read nothing.  As
+// instructions of its own, out of the compiler's sight: it would make LDS reads of other
+// blocks wait for these loads.  meet() waits for them; they write no register.
+template <int kBytes>
+__device__ __forceinline__ void load_to_lds(void *to, const void *from, int bytes, int offset) {
+    const uint64_t base = (uint64_t)from;
+    const u32x4 descriptor = {(unsigned)__builtin_amdgcn_readfirstlane((int)(unsigned)base),
+                              (unsigned)__builtin_amdgcn_readfirstlane((int)((base >> 32) & 0xFFFF)),
+                              (unsigned)__builtin_amdgcn_readfirstlane(max(bytes, 0)), 0x00020000u};
+    const int at = __builtin_amdgcn_readfirstlane((int)(unsigned)(uintptr_t)(lds_void *)to);
+    // the wait states between scalar writes and the load that reads them
+    if constexpr (kBytes == 16)
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+                     : : "s"(at), "v"(offset), "s"(descriptor) : "memory", "m0");
+    else
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dword %1, %2, 0 offen lds"
+                     : : "s"(at), "v"(offset), "s"(descriptor) : "memory", "m0");
+}
+
+// A meeting of the workgroup's wavefronts, each with at most kLeft of its loads into LDS
+// on their way: the barrier alone waits for a wavefront's LDS reads and writes, not for
+// those loads.
+template <int kLeft>
 __device__ __forceinline__ void meet() {
-    __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0)
+    static_assert(kLeft < 64, "six bits");
+    __builtin_amdgcn_s_waitcnt(0x0F70 | (kLeft & 15) | (kLeft >> 4) << 14);  // vmcnt(kLeft)
     __syncthreads();
 }
 
@@ -142,6 +172,7 @@ template <typename S, int kFmtA, int kFmtB, bool kTiles, bool kPrecise>
 struct Tile {
     const GemmArgs &p;
     int lane, wave, m0, n0, wm, wn, row16, quarter;
+    int low_a, high_a, low_b, high_b;  // a lane's two chunks of its wavefront's first 16 rows in LDS
     int offset_a, offset_b;  // of a lane's 16 bytes from the 8 rows that its wavefront loads at once
     const uint8_t *from_a, *from_b;  // the tile's rows
     int bytes_a, bytes_b;            // to the end of their last one's last whole 16 bytes
@@ -156,6 +187,13 @@ struct Tile {
         wn = wave / S::kWavesM * S::kWaveN;
         row16 = lane & 15;
         quarter = lane >> 4;
+        // a lane's 32 codes of a row: chunks 2 quarter, 2 quarter + 1
+        const int low = row16 * kGroup + 16 * ((2 * quarter) ^ (row16 >> 1));
+        const int high = row16 * kGroup + 16 * ((2 * quarter + 1) ^ (row16 >> 1));
+        low_a = wm * kGroup + low;
+        high_a = wm * kGroup + high;
+        low_b = wn * kGroup + low;
+        high_b = wn * kGroup + high;
         const int wide = (p.K + 15) & ~15;
         from_a = p.a + (int64_t)m0 * p.a_pitch;
         from_b = p.b + (int64_t)n0 * p.b_pitch;
@@ -175,16 +213,12 @@ struct Tile {
     // them and ends with the operand, so rows past its end are not read (what their place
     // in LDS holds only meets outputs that are not stored).
     __device__ __forceinline__ void fetch_rows(u32x4 *to, const uint8_t *from, int bytes, int at, int offset) {
-        const __amdgpu_buffer_rsrc_t r =
-            __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(from) + at, 0, max(bytes - at, 0), 0x00020000);
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void *)to, 16, offset, 0, 0, 0);
+        load_to_lds<16>(to, from + at, bytes - at, offset);
     }
 
     // Queues block kb's loads.
     __device__ __forceinline__ void fetch(Stage<S> &to, int kb) {
-        // (opaque, so that no product of the pitches stays in a register over the loop)
-        int a_pitch = (int)p.a_pitch, b_pitch = (int)p.b_pitch;
-        asm volatile("" : "+s"(a_pitch), "+s"(b_pitch));
+        const int a_pitch = (int)p.a_pitch, b_pitch = (int)p.b_pitch;
 #pragma unroll
         for (int i = 0; i < S::kLoadsA; ++i) {
             const int r = (i * S::kWaves + wave) * 8;
@@ -195,22 +229,19 @@ struct Tile {
             const int r = (i * S::kWaves + wave) * 8;
             fetch_rows(to.b + r * 8, from_b, bytes_b, r * b_pitch + kb * kGroup, offset_b);
         }
-        // 64 scales a wavefront; of b's tiles one for each 128 columns
-        constexpr int kScalesB = kTiles ? (S::kN + kGroup - 1) / kGroup : S::kN;
-#pragma unroll
-        for (int k = 0; k < S::kM; k += kWave)
-            if (wave == k / kWave % S::kWaves) fetch_scales(to.sa + k, p.sa, p.M, kb, m0 + k);
+        // 64 scales a wavefront; of b's tiles one for each 128 columns.  A wavefront without
+        // scales of its own repeats another one's: each has the same number of loads to wait for.
+        constexpr int kCountA = (S::kM + kWave - 1) / kWave;
+        constexpr int kCountB = kTiles ? 1 : (S::kN + kWave - 1) / kWave;
+        static_assert(kCountA + kCountB <= S::kWaves && S::kM % 32 == 0 && S::kN % kGroup == 0, "one load each");
         const int cols = kTiles ? (p.N + kGroup - 1) / kGroup : p.N, c0 = kTiles ? n0 / kGroup : n0;
-#pragma unroll
-        for (int k = 0; k < kScalesB; k += kWave)
-            if (wave == S::kWaves - 1 - k / kWave % S::kWaves) fetch_scales(to.sb + k, p.sb, cols, kb, c0 + k);
+        const int w = min(wave, kCountA + kCountB - 1);
+        const bool of_a = w < kCountA;
+        const int count = of_a ? p.M : cols, at = of_a ? m0 + w * kWave : c0 + (w - kCountA) * kWave;
+        load_to_lds<4>(to.scales + w * kWave, (of_a ? p.sa : p.sb) + (int64_t)kb * count + at,
+                       min(count - at, kWave) * 4, 4 * lane);
     }
-    __device__ __forceinline__ void fetch_scales(float *to, const float *from, int count, int kb, int at) {
-        const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
-            const_cast<float *>(from) + (int64_t)kb * count + at, 0, max(min(count - at, kWave), 0) * 4, 0x00020000);
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void *)to, 4, 4 * lane, 0, 0, 0);
-    }
-
+    static constexpr int kFetched = S::kLoadsA + S::kLoadsB + 1;  // loads of a wavefront and block
     // Clears the codes from K on in the last block.
     __device__ __forceinline__ void clear_tail(Stage<S> &in) {
         const int left = p.K % kGroup;
@@ -228,13 +259,25 @@ struct Tile {
         }
     }
 
-    // Rows row .. row + 15; row is a multiple of 16.
-    template <int kFmt>
-    __device__ __forceinline__ Frag<kFmt, kPrecise> frag(const u32x4 *rows, int row) {
-        const u32x4 *mine = rows + row16 * 8 + row * 8;
-        Frag<kFmt, kPrecise> f;
-        f.set(mine[(2 * quarter) ^ (row16 >> 1)], mine[(2 * quarter + 1) ^ (row16 >> 1)]);
+    // LDS is read at one byte offset from its variable: through longer chains of addresses
+    // the compiler loses sight of the variable, and then waits for every load under way.
+    template <typename T>
+    static __device__ __forceinline__ T at(const Stage<S> &in, int offset) {
+        return *reinterpret_cast<const T *>(reinterpret_cast<const char *>(&in) + offset);
+    }
+    static constexpr int kA = (int)__builtin_offsetof(Stage<S>, a), kB = (int)__builtin_offsetof(Stage<S>, b);
+    __device__ __forceinline__ Frag<kFmtA, kPrecise> frag_a(const Stage<S> &in, int i) {
+        Frag<kFmtA, kPrecise> f;
+        f.set(at<u32x4>(in, low_a + (kA + i * 16 * kGroup)), at<u32x4>(in, high_a + (kA + i * 16 * kGroup)));
         return f;
+    }
+    __device__ __forceinline__ Frag<kFmtB, kPrecise> frag_b(const Stage<S> &in, int j) {
+        Frag<kFmtB, kPrecise> f;
+        f.set(at<u32x4>(in, low_b + (kB + j * 16 * kGroup)), at<u32x4>(in, high_b + (kB + j * 16 * kGroup)));
+        return f;
+    }
+    __device__ __forceinline__ float scale_a(const Stage<S> &in, int i) {
+        return at<float>(in, 4 * (wm + row16) + 64 * i);
     }
 
     // What a block's multiplication begins with, read during the one before it.
@@ -243,18 +286,17 @@ struct Tile {
         Frag<kFmtA, kPrecise> a;
         float sa, sb;
     };
-    __device__ __forceinline__ float scale_a(const Stage<S> &in, int i) { return in.sa[wm + i * 16 + row16]; }
     __device__ __forceinline__ void read_head(const Stage<S> &in, Head &h, int item) {
         if (item == 0) {
-            h.a = frag<kFmtA>(in.a, wm);
+            h.a = frag_a(in, 0);
             h.sa = scale_a(in, 0);
             h.sb = 1.0f;
             if constexpr (kTiles) {
                 static_assert(kGroup % S::kWaveN == 0, "one tile of b's scales per wavefront");
-                h.sb = in.sb[wn / kGroup];
+                h.sb = at<float>(in, 4 * (in.kScalesA + wn / kGroup));
             }
         } else {
-            h.b[item - 1] = frag<kFmtB>(in.b, wn + (item - 1) * 16);
+            h.b[item - 1] = frag_b(in, item - 1);
         }
     }
 
@@ -276,7 +318,7 @@ struct Tile {
     // no wavefront waits for LDS at a block's beginning.  The products run kLag tiles
     // ahead of their scaled addition, so that the vector unit adds one tile while the
     // matrix core works on the next ones.
-    __device__ __forceinline__ void step(Stage<S> &cur, Stage<S> &nxt, Head &h, Head &n, int kb, int blocks) {
+    __device__ __forceinline__ void step(Stage<S> &cur, Stage<S> &nxt, Head &h, Head &n, int kb, int end, bool ragged) {
         constexpr int kLag = 3, kTilesM = S::kTilesM, kTilesN = S::kTilesN;
         constexpr int kCount = kTilesM * kTilesN;
         Frag<kFmtA, kPrecise> fa[kTilesM];
@@ -285,34 +327,34 @@ struct Tile {
         fa[0] = h.a;
         sa[0] = h.sa;
 #pragma unroll
-        for (int j = kHeadB; j < kTilesN; ++j) h.b[j] = frag<kFmtB>(cur.b, wn + j * 16);
+        for (int j = kHeadB; j < kTilesN; ++j) h.b[j] = frag_b(cur, j);
         if constexpr (!kTiles) {
 #pragma unroll
             for (int j = 0; j < kTilesN; ++j)
-                sb[j] = *reinterpret_cast<const f32x4 *>(cur.sb + wn + j * 16 + 4 * quarter);
+                sb[j] = at<f32x4>(cur, 4 * (cur.kScalesA + wn + 4 * quarter) + 64 * j);
         }
-        static_for<kCount + kLag>([&](auto step_of) {
+        static_for<kCount + kLag>([&](auto step_of) FP4Q_INLINE {
             constexpr int t = step_of.value, i = t / kTilesN, j = t % kTilesN;
             if constexpr (j == 0 && i < kMeet) {
                 constexpr int from = i ? rows_read(i - 1) : 1, count = rows_read(i) - from;
-                static_for<count>([&](auto k) {
-                    fa[from + k.value] = frag<kFmtA>(cur.a, wm + (from + k.value) * 16);
+                static_for<count>([&](auto k) FP4Q_INLINE {
+                    fa[from + k.value] = frag_a(cur, from + k.value);
                     sa[from + k.value] = scale_a(cur, from + k.value);
                 });
             }
             if constexpr (t == kMeet * kTilesN) {
-                static_for<kMeet * kTilesN>([&](auto x) { asm volatile("" : "+v"(acc[x.value / kTilesN][x.value % kTilesN])); });
-                meet();
-                if (kb + 2 < blocks) {
+                static_for<kMeet * kTilesN>([&](auto x) FP4Q_INLINE { asm volatile("" : "+v"(acc[x.value / kTilesN][x.value % kTilesN])); });
+                meet<0>();
+                if (kb + 2 < end) {
                     fetch(cur, kb + 2);
-                } else if (kb + 2 == blocks && p.K % kGroup) {
+                } else if (kb + 2 == end && ragged) {
                     clear_tail(nxt);
                     __syncthreads();
                 }
             }
             if constexpr (j == 0 && i >= kMeet && i < kTilesM) {
                 constexpr int from = i > kMeet ? head_read(i - 1) : 0, count = head_read(i) - from;
-                static_for<count>([&](auto k) { read_head(nxt, n, from + k.value); });
+                static_for<count>([&](auto k) FP4Q_INLINE { read_head(nxt, n, from + k.value); });
             }
             if constexpr (t < kCount) d[t % (kLag + 1)] = block_product(h.b[j], fa[i]);
             __builtin_amdgcn_sched_barrier(0);  // the matrix core first
@@ -337,8 +379,9 @@ struct Tile {
     // The sums leave a tile row (16 m) at a time through a part of LDS of the wavefront's
     // own, from four neighbours a lane to whole rows: 16 bytes a lane where the output's
     // rows allow it, else one element a lane.  Nobody reads LDS after the last meeting.
-    __device__ __forceinline__ void store(Stage<S> &room) {
-        using Out = std::conditional_t<kPrecise, float, bf16>;
+    template <typename Out>
+    __device__ __forceinline__ void store(Stage<S> &room, Out *out, bool accumulate) {
+        constexpr bool kFloat = std::is_same_v<Out, float>;
         constexpr int kPer16 = 16 / (int)sizeof(Out), kCols = S::kWaveN;
         constexpr int kPitch = kCols + kPer16;  // elements; the shift keeps rows off each other's banks
         static_assert(S::kWaves * 16 * kPitch * sizeof(Out) <= sizeof(room.a) + sizeof(room.b), "fits the stage");
@@ -352,7 +395,7 @@ struct Tile {
 #pragma unroll
             for (int j = 0; j < S::kTilesN; ++j) {
                 Out *to = mine + row16 * kPitch + j * 16 + 4 * quarter;
-                if constexpr (kPrecise) {
+                if constexpr (kFloat) {
                     *reinterpret_cast<f32x4 *>(to) = acc[i][j];
                 } else {
                     u32x2 w;
@@ -368,8 +411,8 @@ struct Tile {
                     const int r = k * kRows + lane / kLanes, c = lane % kLanes * kPer16;
                     if (m1 + r < p.M && n1 + c < p.N) {
                         u32x4 w = *reinterpret_cast<const u32x4 *>(mine + r * kPitch + c);
-                        u32x4 *to = reinterpret_cast<u32x4 *>(static_cast<Out *>(p.out) + (int64_t)(m1 + r) * p.N + n1 + c);
-                        if (kPrecise && p.accumulate) {
+                        u32x4 *to = reinterpret_cast<u32x4 *>(out + (int64_t)(m1 + r) * p.N + n1 + c);
+                        if (kFloat && accumulate) {
                             const u32x4 had = *to;
 #pragma unroll
                             for (int e = 0; e < 4; ++e)
@@ -379,13 +422,14 @@ struct Tile {
                     }
                 }
             } else {
-                static_assert(kCols == kWave, "a lane for each column");
-                for (int r = 0; r < 16 && m1 + r < p.M; ++r)
-                    if (n1 + lane < p.N) {
-                        Out *to = static_cast<Out *>(p.out) + (int64_t)(m1 + r) * p.N + n1 + lane;
-                        Out v = mine[r * kPitch + lane];
-                        if constexpr (kPrecise)
-                            if (p.accumulate) v = *to + v;
+                constexpr int kRows = kWave / kCols;
+                const int c = lane % kCols;
+                for (int r = lane / kCols; r < 16 && m1 + r < p.M; r += kRows)
+                    if (n1 + c < p.N) {
+                        Out *to = out + (int64_t)(m1 + r) * p.N + n1 + c;
+                        Out v = mine[r * kPitch + c];
+                        if constexpr (kFloat)
+                            if (accumulate) v = *to + v;
                         *to = v;
                     }
             }
@@ -401,35 +445,76 @@ __global__ __launch_bounds__(S::kThreads, 2) void gemm_kernel(GemmArgs p) {
     // consecutive workgroups go to the 8 XCDs in turn: each XCD takes a run of tiles,
     // and a run walks 8 tiles of m before it steps in n, so that the tiles that an XCD
     // works on at one time share their operands in its L2
-    const int count = p.tiles_m * p.tiles_n, each = count / 8, more = count % 8;
+    const int tiles = p.tiles_m * p.tiles_n;
+    const int count = tiles * p.parts, each = count / 8, more = count % 8;
     const int xcd = (int)blockIdx.x % 8, turn = (int)blockIdx.x / 8;
-    const int at = xcd * each + min(xcd, more) + turn;
+    const int index = xcd * each + min(xcd, more) + turn;
+    const int part = __builtin_amdgcn_readfirstlane(index / tiles), at = index - part * tiles;
     const int band = at / (8 * p.tiles_n), in_band = at - band * 8 * p.tiles_n;
     const int high = min(8, p.tiles_m - band * 8);
     // (the divisions leave uniform values in vector registers; descriptors need scalars)
     const int tm = __builtin_amdgcn_readfirstlane(band * 8 + in_band % high);
     const int tn = __builtin_amdgcn_readfirstlane(in_band / high);
     Tile<S, kFmtA, kFmtB, kTiles, kPrecise> t(p, tm, tn);
-    const int blocks = (p.K + kGroup - 1) / kGroup, ragged = p.K % kGroup;
-    if (blocks) {
+    const int blocks = (p.K + kGroup - 1) / kGroup;
+    int kb = __builtin_amdgcn_readfirstlane((int)((int64_t)blocks * part / p.parts));
+    const int end = __builtin_amdgcn_readfirstlane((int)((int64_t)blocks * (part + 1) / p.parts));
+    const bool ragged = end == blocks && p.K % kGroup;
+    if (kb < end) {
         typename decltype(t)::Head h0, h1;
-        int kb = 0;
-        t.fetch(even, 0);
-        if (blocks > 1) t.fetch(odd, 1);
-        meet();
-        if (blocks == 1 && ragged) {
-            t.clear_tail(even);
-            __syncthreads();
+        t.fetch(even, kb);
+        if (kb + 1 < end) {
+            t.fetch(odd, kb + 1);
+            meet<t.kFetched>();
+        } else {
+            meet<0>();
+            if (ragged) {
+                t.clear_tail(even);
+                __syncthreads();
+            }
         }
-#pragma unroll
-        for (int i = 0; i <= t.kHeadB; ++i) t.read_head(even, h0, i);
-        for (; kb + 1 < blocks; kb += 2) {
-            t.step(even, odd, h0, h1, kb, blocks);
-            t.step(odd, even, h1, h0, kb + 1, blocks);
+        static_for<t.kHeadB + 1>([&](auto i) FP4Q_INLINE { t.read_head(even, h0, i.value); });
+        for (; kb + 1 < end; kb += 2) {
+            t.step(even, odd, h0, h1, kb, end, ragged);
+            t.step(odd, even, h1, h0, kb + 1, end, ragged);
         }
-        if (kb < blocks) t.step(even, odd, h0, h1, kb, blocks);
+        if (kb < end) t.step(even, odd, h0, h1, kb, end, ragged);
     }
-    t.store(even);
+    if (p.parts > 1)
+        t.store(even, p.partial + part * p.part_size, false);
+    else if constexpr (kPrecise)
+        t.store(even, static_cast<float *>(p.out), p.accumulate);
+    else
+        t.store(even, static_cast<bf16 *>(p.out), false);
+}
+
+// Adds the runs' sums in their order, four neighbours a thread.
+constexpr int kJoinThreads = 256;
+template <typename Out>
+__global__ __launch_bounds__(kJoinThreads) void join_kernel(const float *partial, int64_t part_size, int parts,
+                                                            int64_t count, Out *out, int accumulate) {
+    const int64_t at = ((int64_t)blockIdx.x * kJoinThreads + threadIdx.x) * 4;
+    if (at >= count) return;
+    f32x4 sum = *reinterpret_cast<const f32x4 *>(partial + at);
+    for (int s = 1; s < parts; ++s) sum += *reinterpret_cast<const f32x4 *>(partial + s * part_size + at);
+    if (at + 4 <= count) {
+        if constexpr (std::is_same_v<Out, float>) {
+            f32x4 *to = reinterpret_cast<f32x4 *>(out + at);
+            *to = accumulate ? *to + sum : sum;
+        } else {
+            u32x2 w;
+            w[0] = fp4q_num::bf16_rne_pair(sum[0], sum[1]);
+            w[1] = fp4q_num::bf16_rne_pair(sum[2], sum[3]);
+            *reinterpret_cast<u32x2 *>(out + at) = w;
+        }
+    } else {
+        for (int e = 0; at + e < count; ++e) {
+            if constexpr (std::is_same_v<Out, float>)
+                out[at + e] = accumulate ? out[at + e] + sum[e] : sum[e];
+            else
+                out[at + e] = from_float<bf16>(sum[e]);
+        }
+    }
 }
 
 // 16 bytes of a row at byte k of K: zero from K on.
@@ -462,7 +547,7 @@ __global__ __launch_bounds__(S::kThreads) void strip_kernel(GemmArgs p) {
     const int lane = threadIdx.x & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int row16 = lane & 15, quarter = lane >> 4;
-    const int n0 = (int)blockIdx.x * S::kN;
+    const int n0 = (int)blockIdx.x * S::kN;  // (one tile in m)
     const int blocks = (p.K + kGroup - 1) / kGroup;
     const int cols_sb = kTiles ? (p.N + kGroup - 1) / kGroup : p.N;
     const uint8_t *a[S::kMT], *b[S::kNT];
@@ -559,12 +644,12 @@ __global__ __launch_bounds__(S::kThreads) void strip_kernel(GemmArgs p) {
     }
 }
 
-using Large = Shape<2, 4, 8, 4>;
-using LargePrecise = Shape<2, 4, 4, 4>;
+using Large = Shape<2, 4, 8, 4>;         // 256 x 256, a workgroup a CU
+using LargePrecise = Shape<2, 4, 4, 4>;  // 128 x 256
+using Medium = Shape<2, 2, 4, 4>;        // 128 x 128, two workgroups a CU
+using Low64 = Shape<2, 2, 2, 4>;         // 64 x 128
+using Low32 = Shape<1, 4, 2, 2>;         // 32 x 128
 using Strip16 = Strip<1, 1, 16, 4>;
-using Strip32 = Strip<2, 2, 8, 2>;
-using Strip64 = Strip<4, 2, 8, 2>;
-using Small = Shape<2, 2, 4, 4>;
 
 template <typename S, int kFmtA, int kFmtB, bool kTiles, bool kPrecise>
 struct Kernel {
@@ -589,20 +674,83 @@ const void *pick(int fa, int fb, bool tiles) {
                            : pick<S, kPrecise, FP4Q_E5M2, FP4Q_E5M2>(tiles);
 }
 
+enum class Way { kStrip, kLow32, kLow64, kMedium, kLarge };
+struct Plan {
+    Way way;
+    int tile_m, tile_n, parts;
+    int64_t part_size;
+    size_t workspace;
+};
+
+// The tile and the number of runs that K is cut into: the least of an estimate made of
+// what the kernels take on this card.  A tile's block costs block_us with one, two or
+// three workgroups on a CU (measured at K = 4096 and 8192 with 256, 512 and 768 tiles; a
+// workgroup's beginning and end cost start_us besides), so large tiles serve large
+// outputs (8192 x 11008, K = 4096: 366 us in 256 x 256 tiles, 421 us in 128 x 128) and
+// small ones fill the card when the output is small (1000 x 4096, K = 4096: 27 us in
+// 64 x 128 tiles, 39 us in 256 x 256).  Cutting K fills it further, for a second launch
+// and one write and read of every run's sums (32 x 4096, K = 4096: 11 us in 4 runs, 19 us
+// in one; 4096 x 4096, K = 4096: 109 us in 2 runs, 69 us in one).
+constexpr int kCus = 256;
+Plan plan_of(int64_t M, int64_t N, int64_t K, bool precise) {
+    Plan plan = {Way::kStrip, 16, 16, 1, 0, 0};
+    if (M <= 16) return plan;
+    struct Kind {
+        Way way;
+        int m, n, per_cu;
+        double start_us, block_us[3];
+    };
+    static const Kind fast[] = {{Way::kLow32, 32, 128, 3, 2.5, {0.48, 0.53, 0.69}},
+                                {Way::kLow64, 64, 128, 3, 2.5, {0.54, 0.74, 1.0}},
+                                {Way::kMedium, 128, 128, 2, 4.0, {0.72, 1.13}},
+                                {Way::kLarge, 256, 256, 1, 5.5, {1.75}}};
+    static const Kind exact[] = {{Way::kLow32, 32, 128, 3, 2.5, {0.66, 0.82, 1.1}},
+                                 {Way::kLow64, 64, 128, 2, 2.5, {0.94, 1.23}},
+                                 {Way::kMedium, 128, 128, 2, 4.0, {1.4, 1.98}},
+                                 {Way::kLarge, 128, 256, 1, 5.5, {2.0}}};
+    constexpr double kLaunchUs = 2.5, kJoinUsPerSum = 0.95e-6;
+    const int64_t blocks = ceil_div(K, kGroup);
+    double best = 1e300;
+    for (const Kind &k : precise ? exact : fast) {
+        const int64_t tiles = ceil_div(M, k.m) * ceil_div(N, k.n);
+        for (int parts = 1; parts <= 16 && (parts == 1 || parts * 2 <= blocks); ++parts) {
+            const int64_t all = tiles * parts, full = all / (kCus * k.per_cu), rest = all % (kCus * k.per_cu);
+            const double run = (double)ceil_div(blocks, parts);
+            double us = kLaunchUs + full * (k.start_us + run * k.block_us[k.per_cu - 1]);
+            if (rest) us += k.start_us + run * k.block_us[ceil_div(rest, kCus) - 1];
+            if (parts > 1) us += kLaunchUs + kJoinUsPerSum * M * N * parts;
+            if (us < best) {
+                best = us;
+                plan.way = k.way;
+                plan.tile_m = k.m;
+                plan.tile_n = k.n;
+                plan.parts = parts;
+            }
+        }
+    }
+    if (plan.parts > 1) {
+        plan.part_size = ceil_div(M * N, 4) * 4;
+        plan.workspace = (size_t)(plan.part_size * plan.parts) * 4;
+    }
+    return plan;
+}
+
 bool bad_gemm(int64_t M, int64_t N, int64_t K) {
     return M < 0 || N < 0 || K < 0 || M >= kDimLimit || N >= kDimLimit || K >= kDimLimit ||
-           ceil_div(M, Small::kM) * ceil_div(N, Small::kN) > (int64_t)0x7FFFFFFF;
+           ceil_div(M, 32) * ceil_div(N, 128) > (int64_t)0x7FFFFFFF / 16;
 }
 
 }  // namespace
 
 extern "C" {
 
-int fp4q_gemm8_workspace(int64_t M, int64_t N, int64_t K, uint32_t flags, size_t *bytes) {
+int fp4q_gemm8_workspace(int64_t M, int64_t N, int64_t K, int out_dtype, uint32_t flags, size_t *bytes) {
     if (bad_gemm(M, N, K)) return FP4Q_ERR_SHAPE;
     if (flags & ~(uint32_t)(FP4Q_FLAG_TILES | FP4Q_FLAG_ACCUMULATE)) return FP4Q_ERR_ARG;
+    if (out_dtype != FP4Q_OUT_F32 && (out_dtype != FP4Q_OUT_BF16 || (flags & FP4Q_FLAG_ACCUMULATE)))
+        return FP4Q_ERR_ARG;
     if (!bytes) return FP4Q_ERR_NULL;
-    *bytes = 0;
+    *bytes = M && N ? plan_of(M, N, K, out_dtype == FP4Q_OUT_F32).workspace : 0;
     return FP4Q_OK;
 }
 
@@ -613,10 +761,9 @@ int fp4q_gemm8(const uint8_t *a, int64_t a_pitch, int a_format, const float *a_s
     size_t need = 0;
     if (bad_gemm(M, N, K)) return FP4Q_ERR_SHAPE;
     if (K > 0 && (a_pitch < K || b_pitch < K || a_pitch >= (1 << 23) || b_pitch >= (1 << 23))) return FP4Q_ERR_SHAPE;
-    const int st = fp4q_gemm8_workspace(M, N, K, flags, &need);
+    const int st = fp4q_gemm8_workspace(M, N, K, out_dtype, flags, &need);
     if (st != FP4Q_OK) return st;
     const bool add = flags & FP4Q_FLAG_ACCUMULATE, tiles = flags & FP4Q_FLAG_TILES;
-    if (out_dtype != FP4Q_OUT_F32 && (out_dtype != FP4Q_OUT_BF16 || add)) return FP4Q_ERR_ARG;
     if ((a_format != FP4Q_E4M3 && a_format != FP4Q_E5M2) || (b_format != FP4Q_E4M3 && b_format != FP4Q_E5M2))
         return FP4Q_ERR_ARG;
     if (M == 0 || N == 0) return FP4Q_OK;
@@ -631,27 +778,34 @@ int fp4q_gemm8(const uint8_t *a, int64_t a_pitch, int a_format, const float *a_s
                          rng(a_scales, 4 * groups * M),
                          rng(b_scales, 4 * groups * (tiles ? ceil_div(N, kGroup) : N))};
     if (clash(outs, 2, ins, K > 0 ? 4 : 0)) return FP4Q_ERR_ARG;
+    const bool precise = out_dtype == FP4Q_OUT_F32;
+    const Plan plan = plan_of(M, N, K, precise);
     GemmArgs p = {a, b, a_scales, b_scales, out, a_pitch, b_pitch, (int)M, (int)N, (int)K,
-                  0, 0, out_dtype == FP4Q_OUT_F32, add};
+                  (int)ceil_div(M, plan.tile_m), (int)ceil_div(N, plan.tile_n), precise, add,
+                  plan.parts, plan.part_size, static_cast<float *>(workspace)};
     void *args[] = {&p};
-    const bool precise = p.out_f32;
-    if (M <= 64) {
-        auto strip = [&](auto shape) {
-            using S = decltype(shape);
-            return launch(precise ? pick<S, true>(a_format, b_format, tiles) : pick<S, false>(a_format, b_format, tiles),
-                          dim3((unsigned)ceil_div(N, S::kN)), S::kThreads, args, stream);
-        };
-        return M <= 16 ? strip(Strip16{}) : M <= 32 ? strip(Strip32{}) : strip(Strip64{});
+    const void *fn = nullptr;
+    int threads = 0;
+    auto use = [&](auto fast, auto exact) {
+        using Fast = decltype(fast);
+        using Exact = decltype(exact);
+        static_assert(Fast::kThreads == Exact::kThreads, "one launch for both");
+        fn = precise ? pick<Exact, true>(a_format, b_format, tiles) : pick<Fast, false>(a_format, b_format, tiles);
+        threads = Fast::kThreads;
+    };
+    switch (plan.way) {
+        case Way::kStrip: use(Strip16{}, Strip16{}); break;
+        case Way::kLow32: use(Low32{}, Low32{}); break;
+        case Way::kLow64: use(Low64{}, Low64{}); break;
+        case Way::kMedium: use(Medium{}, Medium{}); break;
+        case Way::kLarge: use(Large{}, LargePrecise{}); break;
     }
-    const int lm = precise ? LargePrecise::kM : Large::kM, ln = precise ? LargePrecise::kN : Large::kN;
-    const bool large = ceil_div(M, lm) * ceil_div(N, ln) >= 200;
-    p.tiles_m = (int)ceil_div(M, large ? lm : Small::kM);
-    p.tiles_n = (int)ceil_div(N, large ? ln : Small::kN);
-    const void *fn = large ? precise ? pick<LargePrecise, true>(a_format, b_format, tiles)
-                                     : pick<Large, false>(a_format, b_format, tiles)
-                   : precise ? pick<Small, true>(a_format, b_format, tiles)
-                             : pick<Small, false>(a_format, b_format, tiles);
-    return launch(fn, dim3((unsigned)(p.tiles_m * p.tiles_n)), large ? 512 : 256, args, stream);
+    const int done = launch(fn, dim3((unsigned)(p.tiles_m * p.tiles_n * p.parts)), threads, args, stream);
+    if (plan.parts == 1 || done != FP4Q_OK) return done;
+    int64_t count = M * N;
+    void *join_args[] = {&p.partial, &p.part_size, &p.parts, &count, &out, &p.accumulate};
+    return launch(precise ? (const void *)&join_kernel<float> : (const void *)&join_kernel<bf16>,
+                  dim3((unsigned)ceil_div(count, 4 * kJoinThreads)), kJoinThreads, join_args, stream);
 }
 
 }  // extern "C"

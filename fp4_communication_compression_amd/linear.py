@@ -41,7 +41,7 @@ def _lib() -> ctypes.CDLL:
         L.fp4q_rmsnorm_backward_workspace.argtypes = [I64, I64, SZ]
         L.fp4q_rmsnorm_backward.argtypes = [P, P, P, P, P, I64, I64, I, P, P, P, Z, P]
         L.fp4q_quantize8.argtypes = [P, I64, I64, I, I, P, I64, P, P, I64, P, U32, P]
-        L.fp4q_gemm8_workspace.argtypes = [I64, I64, I64, U32, SZ]
+        L.fp4q_gemm8_workspace.argtypes = [I64, I64, I64, I, U32, SZ]
         L.fp4q_gemm8.argtypes = [P, I64, I, P, P, I64, I, P, I64, I64, I64, P, I, U32, P, Z, P]
         _bound = L
     return L
@@ -269,7 +269,7 @@ def fp4q_gemm8(a, a_scales, b, b_scales, out=None, out_dtype=None, accumulate: b
         raise TypeError("fp4q: out must be float32%s, got %s" % ("" if accumulate else " or bfloat16", dtype))
     gpu = _gpu(a, a_scales, b, b_scales, out)
     flags = (FP4Q_FLAG_TILES if tiles else 0) | (FP4Q_FLAG_ACCUMULATE if accumulate else 0)
-    need = _workspace("fp4q_gemm8_workspace", M, N, K, flags)
+    need = _workspace("fp4q_gemm8_workspace", M, N, K, code, flags)
     if out is None:
         out = _empty((M, N), dtype, gpu, stream)
     space = _empty((need,), torch.uint8, gpu, stream) if need else None

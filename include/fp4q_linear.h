@@ -114,7 +114,7 @@ int fp4q_quantize8(const void *x, int64_t rows, int64_t cols, int dtype, int for
  *               FP4Q_FLAG_ACCUMULATE (fp32 only) added to
  *   workspace   fp4q_gemm8_workspace bytes of scratch memory (NULL if 0)
  * 0 <= M, N, K < 2^28, pitches < 2^23. */
-int fp4q_gemm8_workspace(int64_t M, int64_t N, int64_t K, uint32_t flags, size_t *bytes);
+int fp4q_gemm8_workspace(int64_t M, int64_t N, int64_t K, int out_dtype, uint32_t flags, size_t *bytes);
 int fp4q_gemm8(const uint8_t *a, int64_t a_pitch, int a_format, const float *a_scales,
                const uint8_t *b, int64_t b_pitch, int b_format, const float *b_scales, int64_t M,
                int64_t N, int64_t K, void *out, int out_dtype, uint32_t flags, void *workspace,

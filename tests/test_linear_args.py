@@ -220,8 +220,10 @@ def test_workspace_sizes():
     assert L.fp4q_rmsnorm_backward_workspace(4, 0, ctypes.byref(size)) == SHAPE
     assert L.fp4q_rmsnorm_backward_workspace(4, 8, None) == NULL
     assert L.fp4q_rmsnorm_backward_workspace(0, 8, ctypes.byref(size)) == OK and size.value == 0
-    assert L.fp4q_gemm8_workspace(4, 4, 4, 8, ctypes.byref(size)) == ARG
-    assert L.fp4q_gemm8_workspace(-1, 4, 4, 0, ctypes.byref(size)) == SHAPE
-    assert L.fp4q_gemm8_workspace(4, 4, 4, 0, None) == NULL
-    assert L.fp4q_gemm8_workspace(0, 4, 4, 0, ctypes.byref(size)) == OK and size.value == 0
-    assert L.fp4q_gemm8_workspace(1 << 27, 1 << 27, 1, 0, ctypes.byref(size)) == SHAPE
+    assert L.fp4q_gemm8_workspace(4, 4, 4, 1, 8, ctypes.byref(size)) == ARG
+    assert L.fp4q_gemm8_workspace(4, 4, 4, 2, 0, ctypes.byref(size)) == ARG
+    assert L.fp4q_gemm8_workspace(4, 4, 4, 1, 4, ctypes.byref(size)) == ARG
+    assert L.fp4q_gemm8_workspace(-1, 4, 4, 1, 0, ctypes.byref(size)) == SHAPE
+    assert L.fp4q_gemm8_workspace(4, 4, 4, 1, 0, None) == NULL
+    assert L.fp4q_gemm8_workspace(0, 4, 4, 1, 0, ctypes.byref(size)) == OK and size.value == 0
+    assert L.fp4q_gemm8_workspace(1 << 27, 1 << 27, 1, 1, 0, ctypes.byref(size)) == SHAPE
