@@ -7,6 +7,8 @@
 
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "fp4q_linear.h"
 #include "fp4q_numerics.h"
 
@@ -32,52 +34,92 @@ __device__ __forceinline__ bf16 from_float<bf16>(float v) {
     return bf16{(uint16_t)fp4q_num::bf16_rne_pair(v, v)};
 }
 
-// Eight consecutive elements, 16-byte aligned: one load of bf16, two of fp32.
+// 16 bytes at an element's alignment: one load or store all the same (rows of an odd
+// length begin anywhere).
 template <typename T>
-struct Eight;
+struct Loose;
 template <>
-struct Eight<bf16> {
-    u32x4 w;
-    __device__ __forceinline__ void load(const bf16 *p) { w = *reinterpret_cast<const u32x4 *>(p); }
-    __device__ __forceinline__ void zero() { w = u32x4{0, 0, 0, 0}; }
-    __device__ __forceinline__ void get(float (&v)[8]) const {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            v[2 * i] = __uint_as_float(w[i] << 16);
-            v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-        }
-    }
-    __device__ __forceinline__ void set(const float (&v)[8]) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = fp4q_num::bf16_rne_pair(v[2 * i], v[2 * i + 1]);
-    }
-    __device__ __forceinline__ void store(bf16 *p) const { *reinterpret_cast<u32x4 *>(p) = w; }
+struct Loose<bf16> {
+    typedef u32x4 Vec __attribute__((aligned(2)));
 };
 template <>
-struct Eight<float> {
-    u32x4 a, b;
-    __device__ __forceinline__ void load(const float *p) {
-        a = reinterpret_cast<const u32x4 *>(p)[0];
-        b = reinterpret_cast<const u32x4 *>(p)[1];
+struct Loose<float> {
+    typedef u32x4 Vec __attribute__((aligned(4)));
+};
+
+// Eight consecutive elements as they lie in memory.  With kWhole, p is 16-byte aligned and
+// all eight exist or none; otherwise the first `left` exist.
+template <typename T>
+struct Eight {
+    static constexpr int kWords = 2 * (int)sizeof(T);
+    unsigned w[kWords];
+
+    template <bool kWhole>
+    __device__ __forceinline__ void load(const T *p, int left) {
+        using Vec = std::conditional_t<kWhole, u32x4, typename Loose<T>::Vec>;
+        if (left >= 8) {
+#pragma unroll
+            for (int k = 0; k < kWords / 4; ++k) {
+                const u32x4 v = reinterpret_cast<const Vec *>(p)[k];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) w[4 * k + i] = v[i];
+            }
+            return;
+        }
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) w[i] = 0;
+        if (!kWhole) {
+#pragma unroll
+            for (int i = 0; i < 7; ++i)
+                if (i < left) put(i, p[i]);
+        }
     }
-    __device__ __forceinline__ void zero() { a = b = u32x4{0, 0, 0, 0}; }
+    template <bool kWhole>
+    __device__ __forceinline__ void store(T *p, int left) const {
+        using Vec = std::conditional_t<kWhole, u32x4, typename Loose<T>::Vec>;
+        if (left >= 8) {
+#pragma unroll
+            for (int k = 0; k < kWords / 4; ++k)
+                reinterpret_cast<Vec *>(p)[k] = u32x4{w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]};
+        } else if (!kWhole) {
+#pragma unroll
+            for (int i = 0; i < 7; ++i)
+                if (i < left) p[i] = pick(i);
+        }
+    }
     __device__ __forceinline__ void get(float (&v)[8]) const {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            v[i] = __uint_as_float(a[i]);
-            v[4 + i] = __uint_as_float(b[i]);
-        }
+        for (int i = 0; i < 8; ++i) v[i] = to_float(pick(i));
     }
     __device__ __forceinline__ void set(const float (&v)[8]) {
+        if constexpr (sizeof(T) == 4) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            a[i] = __float_as_uint(v[i]);
-            b[i] = __float_as_uint(v[4 + i]);
+            for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(v[i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = fp4q_num::bf16_rne_pair(v[2 * i], v[2 * i + 1]);
         }
     }
-    __device__ __forceinline__ void store(float *p) const {
-        reinterpret_cast<u32x4 *>(p)[0] = a;
-        reinterpret_cast<u32x4 *>(p)[1] = b;
+
+    // Hides the words' origin: what was computed from them before is computed again rather
+    // than held in registers.
+    __device__ __forceinline__ void forget() {
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) asm volatile("" : "+v"(w[i]));
+    }
+
+   private:
+    __device__ __forceinline__ void put(int i, T v) {
+        if constexpr (sizeof(T) == 4)
+            w[i] = __float_as_uint(v);
+        else
+            w[i >> 1] |= (unsigned)v.bits << (16 * (i & 1));
+    }
+    __device__ __forceinline__ T pick(int i) const {
+        if constexpr (sizeof(T) == 4)
+            return __uint_as_float(w[i]);
+        else
+            return bf16{(uint16_t)(w[i >> 1] >> (16 * (i & 1)))};
     }
 };
 
@@ -116,6 +158,15 @@ __device__ __forceinline__ unsigned code_pair(unsigned old, float v0, float v1, 
 template <int kFmt>
 __device__ __forceinline__ unsigned code_quad(float v0, float v1, float v2, float v3, Scale sc) {
     return code_pair<kFmt, true>(code_pair<kFmt, false>(0u, v0, v1, sc), v2, v3, sc);
+}
+
+// The first min(left, 8) bytes of w; p is 8-byte aligned.
+__device__ __forceinline__ void store_bytes8(uint8_t *p, int left, u32x2 w) {
+    if (left >= 8) {
+        *reinterpret_cast<u32x2 *>(p) = w;
+    } else {
+        for (int j = 0; j < left; ++j) p[j] = (uint8_t)(w[j >> 2] >> (8 * (j & 3)));
+    }
 }
 
 // --------------------------------------------------------- lane reductions

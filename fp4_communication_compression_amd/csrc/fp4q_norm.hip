@@ -14,6 +14,8 @@ namespace {
 
 using namespace fp4q_f8;
 
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
 // Sum of one value per lane over the kWaves wavefronts that share a row.
 // `lds` holds kWaves floats per row and call.
 template <int kWaves>
@@ -43,10 +45,10 @@ struct NormArgs {
     int rows, cols;
 };
 
-// Rows of whole 16-byte chunks.  kWaves wavefronts share a row, each lane holds
-// kChunks chunks of 8 elements; a 128-group is 16 neighbouring lanes, so its
-// maximum is four DPP steps.
-template <typename T, int kWaves, int kChunks>
+// kWaves wavefronts share a row, each lane holds kChunks chunks of 8 elements; a 128-group
+// is 16 neighbouring lanes, so its maximum is four DPP steps.  kWhole: rows of whole
+// 16-byte chunks; otherwise chunks lie at any element and the last one may be shorter.
+template <typename T, int kWaves, int kChunks, bool kWhole>
 __global__ __launch_bounds__(kWaves == 1 ? 256 : kWaves * kWave) void norm_kernel(NormArgs a) {
     constexpr int kRows = kWaves == 1 ? 4 : 1;
     __shared__ float lds[kWaves];
@@ -55,36 +57,30 @@ __global__ __launch_bounds__(kWaves == 1 ? 256 : kWaves * kWave) void norm_kerne
     const int part = kWaves == 1 ? 0 : wave;
     const int row = (int)blockIdx.x * kRows + (kWaves == 1 ? wave : 0);
     if (row >= a.rows) return;  // whole wavefronts, and no barrier with kWaves == 1
-    const int chunks = a.cols / 8;
     const int64_t base = (int64_t)row * a.cols;
-    const T *x = static_cast<const T *>(a.x) + base;
+    const int first = 8 * (part * kWave + lane);  // element of chunk 0; chunk c is kStep c further
+    constexpr int kStep = 8 * kWaves * kWave;
 
     Eight<T> in[kChunks];
     float v[kChunks][8];
 #pragma unroll
-    for (int c = 0; c < kChunks; ++c) {
-        const int k = (c * kWaves + part) * kWave + lane;
-        if (k < chunks) in[c].load(x + 8 * k); else in[c].zero();
-    }
+    for (int c = 0; c < kChunks; ++c)
+        in[c].template load<kWhole>(static_cast<const T *>(a.x) + base + first + c * kStep, a.cols - first - c * kStep);
     if (a.residual) {
-        const T *res = static_cast<const T *>(a.residual) + base;
-        T *h = static_cast<T *>(a.h) + base;
         Eight<T> add[kChunks];
 #pragma unroll
-        for (int c = 0; c < kChunks; ++c) {
-            const int k = (c * kWaves + part) * kWave + lane;
-            if (k < chunks) add[c].load(res + 8 * k); else add[c].zero();
-        }
+        for (int c = 0; c < kChunks; ++c)
+            add[c].template load<kWhole>(static_cast<const T *>(a.residual) + base + first + c * kStep,
+                                         a.cols - first - c * kStep);
 #pragma unroll
         for (int c = 0; c < kChunks; ++c) {
-            const int k = (c * kWaves + part) * kWave + lane;
             float p[8], q[8];
             in[c].get(p);
             add[c].get(q);
 #pragma unroll
             for (int i = 0; i < 8; ++i) p[i] += q[i];
             in[c].set(p);  // the norm is taken of the stored sum
-            if (k < chunks) in[c].store(h + 8 * k);
+            in[c].template store<kWhole>(static_cast<T *>(a.h) + base + first + c * kStep, a.cols - first - c * kStep);
         }
     }
     float sumsq = 0.0f;
@@ -97,13 +93,12 @@ __global__ __launch_bounds__(kWaves == 1 ? 256 : kWaves * kWave) void norm_kerne
     const float r = rstd_of(row_sum<kWaves>(sumsq, lds, part), a.cols, a.eps);
     if (a.rstd && threadIdx.x % (kWaves * kWave) == 0) a.rstd[row] = r;
 
-    const T *w = static_cast<const T *>(a.weight);
 #pragma unroll
     for (int c = 0; c < kChunks; ++c) {
-        const int k = (c * kWaves + part) * kWave + lane;
-        const bool valid = k < chunks;
+        const int at = first + c * kStep, left = a.cols - at;
         Eight<T> wk;
-        if (valid) wk.load(w + 8 * k); else wk.zero();
+        wk.template load<true>(static_cast<const T *>(a.weight) + at, left >= 8 ? 8 : 0);
+        if (!kWhole && left < 8) wk.template load<false>(static_cast<const T *>(a.weight) + at, left);
         float wv[8];
         wk.get(wv);
         unsigned top = 0;
@@ -112,26 +107,26 @@ __global__ __launch_bounds__(kWaves == 1 ? 256 : kWaves * kWave) void norm_kerne
             v[c][i] = v[c][i] * r * wv[i];
             top = umax(top, mag(v[c][i]));
         }
-        if (a.y && valid) {
+        if (a.y) {
             Eight<T> o;
             o.set(v[c]);
-            o.store(static_cast<T *>(a.y) + base + 8 * k);
+            o.template store<kWhole>(static_cast<T *>(a.y) + base + at, left);
         }
         if (a.codes) {
             const Scale sc = scale_of<FP4Q_E4M3>(max16(top));
-            if (valid) {
+            if (left > 0) {
                 u32x2 q;
                 q[0] = code_quad<FP4Q_E4M3>(v[c][0], v[c][1], v[c][2], v[c][3], sc);
                 q[1] = code_quad<FP4Q_E4M3>(v[c][4], v[c][5], v[c][6], v[c][7], sc);
-                *reinterpret_cast<u32x2 *>(a.codes + (int64_t)row * a.code_pitch + 8 * k) = q;
-                if ((lane & 15) == 0) a.scales[(int64_t)(k / 16) * a.rows + row] = sc.s;
+                store_bytes8(a.codes + (int64_t)row * a.code_pitch + at, left, q);
+                if ((lane & 15) == 0) a.scales[(int64_t)(at / kGroup) * a.rows + row] = sc.s;
             }
         }
     }
 }
 
-// Any width: a workgroup per row, a wavefront per 128-group, two passes over the
-// row (the second reads what the same lanes have read or written before).
+// Rows too long for registers: a workgroup per row, a wavefront per 128-group, two passes
+// over the row (the second reads what the same lanes have read or written before).
 constexpr int kAnyWaves = 4;
 template <typename T>
 __global__ __launch_bounds__(kAnyWaves * kWave) void norm_any_kernel(NormArgs a) {
@@ -198,87 +193,120 @@ struct GradArgs {
     int rows, cols;
 };
 
-// Rows of whole chunks.  A workgroup takes rows blockIdx.x, + gridDim.x, ...,
-// and keeps its part of dw in registers over all of them; the parts are added
-// by weight_grad_kernel.
-template <typename T, int kWaves, int kChunks>
-__global__ __launch_bounds__(kWaves * kWave) void norm_grad_kernel(GradArgs a) {
-    __shared__ float lds[2][kWaves];
+// kTeams teams of kWaves wavefronts, a row each at a time; the rows of a workgroup's teams
+// are kTeams blockIdx.x + team, and gridDim.x kTeams further each turn.  The next row's
+// loads are queued before the present row's sum is waited for (kAhead).  Each lane keeps
+// its columns' part of dw in registers over all its rows; a workgroup's teams add theirs
+// through LDS at the end, and weight_grad_kernel adds the workgroups'.
+template <typename T, int kTeams, int kWaves, int kChunks, bool kWhole>
+__global__ __launch_bounds__(kTeams * kWaves * kWave) void norm_grad_kernel(GradArgs a) {
+    constexpr bool kAhead = kChunks == 1;  // where the registers allow it
+    constexpr int kStep = 8 * kWaves * kWave;
+    constexpr int kKept = kTeams > 1 ? (kTeams - 1) * kWaves * kWave * kChunks * 2 : 1;
+    __shared__ f32x4 kept[kKept];
+    __shared__ float lds[2][kTeams][kWaves];
     const int lane = threadIdx.x & (kWave - 1);
-    const int part = threadIdx.x / kWave;
-    const int chunks = a.cols / 8;
-    float dw[kChunks][8], w[kChunks][8];
+    const int wave = threadIdx.x / kWave, team = wave / kWaves, part = wave % kWaves;
+    const int first = 8 * (part * kWave + lane);
+    struct Row {
+        Eight<T> dy[kChunks], h[kChunks], dh[kChunks];
+        float r;
+    };
+    auto load = [&](Row &to, int row) __attribute__((always_inline)) {
+        const bool here = row < a.rows;
+        const int64_t base = (int64_t)(here ? row : 0) * a.cols;
+        to.r = here ? a.rstd[row] : 0.0f;
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c) {
+            const int at = first + c * kStep, left = here ? a.cols - at : 0;
+            to.dy[c].template load<kWhole>(static_cast<const T *>(a.dy) + base + at, left);
+            to.h[c].template load<kWhole>(static_cast<const T *>(a.h) + base + at, left);
+            if (a.dh) to.dh[c].template load<kWhole>(static_cast<const T *>(a.dh) + base + at, left);
+        }
+    };
+    Eight<T> weight[kChunks];
+    float dw[kChunks][8];
 #pragma unroll
     for (int c = 0; c < kChunks; ++c) {
-        const int k = (c * kWaves + part) * kWave + lane;
-        Eight<T> wk;
-        if (k < chunks) wk.load(static_cast<const T *>(a.weight) + 8 * k); else wk.zero();
-        wk.get(w[c]);
+        const int at = first + c * kStep;
+        weight[c].template load<kWhole>(static_cast<const T *>(a.weight) + at, a.cols - at);
 #pragma unroll
         for (int i = 0; i < 8; ++i) dw[c][i] = 0.0f;
     }
-    int turn = 0;
-    for (int row = (int)blockIdx.x; row < a.rows; row += (int)gridDim.x, turn ^= 1) {
-        const int64_t base = (int64_t)row * a.cols;
-        Eight<T> dy[kChunks], h[kChunks], add[kChunks];
-#pragma unroll
-        for (int c = 0; c < kChunks; ++c) {
-            const int k = (c * kWaves + part) * kWave + lane;
-            if (k < chunks) {
-                dy[c].load(static_cast<const T *>(a.dy) + base + 8 * k);
-                h[c].load(static_cast<const T *>(a.h) + base + 8 * k);
-                if (a.dh) add[c].load(static_cast<const T *>(a.dh) + base + 8 * k);
-            } else {
-                dy[c].zero();
-                h[c].zero();
-                add[c].zero();
-            }
-        }
-        const float r = a.rstd[row];
+    const int stride = (int)gridDim.x * kTeams;
+    Row now, next;
+    int row = (int)blockIdx.x * kTeams + team, turn = 0;
+    load(now, row);
+    // every team makes the workgroup's number of turns, for the barrier in row_sum
+    for (int lead = (int)blockIdx.x * kTeams; lead < a.rows; lead += stride, row += stride, turn ^= 1) {
+        if (kAhead) load(next, row + stride);
         float dot = 0.0f;
 #pragma unroll
         for (int c = 0; c < kChunks; ++c) {
-            float p[8], q[8];
-            dy[c].get(p);
-            h[c].get(q);
+            float p[8], q[8], w[8];
+            now.dy[c].get(p);
+            now.h[c].get(q);
+            weight[c].get(w);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const float xhat = q[i] * r;
-                dot = fmaf(p[i] * w[c][i], xhat, dot);
+                const float xhat = q[i] * now.r;
+                dot = fmaf(p[i] * w[i], xhat, dot);
                 dw[c][i] = fmaf(p[i], xhat, dw[c][i]);
             }
         }
-        // two buffers in turn: a row's sums are read before the next barrier,
-        // and written again only after it
-        const float m = row_sum<kWaves>(dot, lds[turn], part) / (float)a.cols;
+        // two buffers in turn: a row's sums are read before the next barrier, and written
+        // again only after it
+        const float m = row_sum<kWaves>(dot, lds[turn][team], part) / (float)a.cols;
+        const int64_t base = (int64_t)row * a.cols;
 #pragma unroll
         for (int c = 0; c < kChunks; ++c) {
-            const int k = (c * kWaves + part) * kWave + lane;
-            float p[8], q[8], s[8] = {};
-            dy[c].get(p);
-            h[c].get(q);
-            if (a.dh) add[c].get(s);
+            now.dy[c].forget();
+            now.h[c].forget();
+            weight[c].forget();
+            float p[8], q[8], w[8], s[8] = {};
+            now.dy[c].get(p);
+            now.h[c].get(q);
+            weight[c].get(w);
+            if (a.dh) now.dh[c].get(s);
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                p[i] = fmaf(r, fmaf(-(q[i] * r), m, p[i] * w[c][i]), s[i]);
+                p[i] = fmaf(now.r, fmaf(-(q[i] * now.r), m, p[i] * w[i]), s[i]);
             Eight<T> o;
             o.set(p);
-            if (k < chunks) o.store(static_cast<T *>(a.dx) + base + 8 * k);
+            const int at = first + c * kStep;
+            o.template store<kWhole>(static_cast<T *>(a.dx) + base + at, row < a.rows ? a.cols - at : 0);
         }
+        if (kAhead) now = next; else load(now, row + stride);
+    }
+    if constexpr (kTeams > 1) {
+        f32x4 *mine = kept + (part * kWave + lane);
+        if (team > 0) {
+#pragma unroll
+            for (int k = 0; k < 2 * kChunks; ++k)
+                mine[((team - 1) * 2 * kChunks + k) * kWaves * kWave] =
+                    f32x4{dw[k / 2][4 * (k % 2)], dw[k / 2][4 * (k % 2) + 1], dw[k / 2][4 * (k % 2) + 2], dw[k / 2][4 * (k % 2) + 3]};
+        }
+        __syncthreads();
+        if (team > 0) return;
+        for (int t = 0; t < kTeams - 1; ++t)
+#pragma unroll
+            for (int k = 0; k < 2 * kChunks; ++k) {
+                const f32x4 v = mine[(t * 2 * kChunks + k) * kWaves * kWave];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) dw[k / 2][4 * (k % 2) + i] += v[i];
+            }
     }
     float *to = a.partial + (int64_t)blockIdx.x * a.cols;
 #pragma unroll
     for (int c = 0; c < kChunks; ++c) {
-        const int k = (c * kWaves + part) * kWave + lane;
-        if (k < chunks) {
-            Eight<float> o;
-            o.set(dw[c]);
-            o.store(to + 8 * k);
-        }
+        const int at = first + c * kStep;
+        Eight<float> o;
+        o.set(dw[c]);
+        o.template store<kWhole>(to + at, a.cols - at);
     }
 }
 
-// Any width: dx a row at a time (two passes over the row) ...
+// Rows too long for registers: dx a row at a time (two passes over the row) ...
 template <typename T>
 __global__ __launch_bounds__(kAnyWaves * kWave) void norm_grad_any_kernel(GradArgs a) {
     __shared__ float lds[kAnyWaves];
@@ -322,61 +350,83 @@ __global__ __launch_bounds__(kAnyWaves * kWave) void weight_grad_any_kernel(Grad
     }
 }
 
-// dw[k] = sum of the parts, in their order: 16 slices of the parts, then those.
-constexpr int kSlices = 16;
-constexpr int kSliceCols = 16;
-__global__ __launch_bounds__(kSlices * kSliceCols) void weight_grad_kernel(const float *partial, int parts,
-                                                                           int cols, float *dweight) {
-    __shared__ float lds[kSlices][kSliceCols];
-    const int lane = threadIdx.x % kSliceCols;
-    const int slice = threadIdx.x / kSliceCols;
-    const int k = (int)blockIdx.x * kSliceCols + lane;
-    float sum = 0.0f;
-    if (k < cols)
-        for (int p = slice; p < parts; p += kSlices) sum += partial[(int64_t)p * cols + k];
-    lds[slice][lane] = sum;
-    __syncthreads();
-    if (slice == 0 && k < cols) {
+// dw = sum of the parts: kSlices slices of them (part p in slice p % kSlices), four columns
+// a thread, then the slices in their order.  A thread's loads do not wait for each other.
+constexpr int kSlices = 32, kSumLanes = 16, kSumCols = 4 * kSumLanes;
+__global__ __launch_bounds__(kSlices * kSumLanes) void weight_grad_kernel(const float *partial, int parts, int cols,
+                                                                          float *dweight) {
+    __shared__ float lds[kSlices][kSumCols];
+    const int lane = threadIdx.x % kSumLanes, slice = threadIdx.x / kSumLanes;
+    const int k = (int)blockIdx.x * kSumCols + 4 * lane;
+    f32x4 sum = {0, 0, 0, 0};
+    if (k + 4 <= cols) {
+#pragma unroll 8
+        for (int p = slice; p < parts; p += kSlices) {
+            const u32x4 v = *reinterpret_cast<const Loose<float>::Vec *>(partial + (int64_t)p * cols + k);
 #pragma unroll
-        for (int i = 1; i < kSlices; ++i) sum += lds[i][lane];
-        dweight[k] = sum;
+            for (int i = 0; i < 4; ++i) sum[i] += __uint_as_float(v[i]);
+        }
+    } else {
+        for (int p = slice; p < parts; p += kSlices)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (k + i < cols) sum[i] += partial[(int64_t)p * cols + k + i];
+    }
+    *reinterpret_cast<f32x4 *>(&lds[slice][4 * lane]) = sum;
+    __syncthreads();
+    const int at = (int)blockIdx.x * kSumCols + (int)threadIdx.x;
+    if (threadIdx.x < kSumCols && at < cols) {
+        float total = lds[0][threadIdx.x];
+#pragma unroll
+        for (int i = 1; i < kSlices; ++i) total += lds[i][threadIdx.x];
+        dweight[at] = total;
     }
 }
 
 // --------------------------------------------------------------------- host
-// The kernel whose lanes hold a row of `cols` elements, and its launch.
+// The kernel whose lanes hold a row of `cols` elements, its workgroup's threads and rows.
 struct Pick {
     const void *fn;
-    int threads, rows_per_wg;
+    int threads, rows;
 };
-constexpr int kWidest = 16 * kWave * 8 * 4;  // 16 wavefronts of 4 chunks
+constexpr int kWidestNorm = 65536, kWidestGrad = 16384;
 
-template <typename T>
+template <typename T, bool kWhole>
 Pick pick_norm(int64_t cols) {
-    const int64_t c = ceil_div(cols / 8, kWave);  // chunks per lane of one wavefront
-    if (c <= 1) return {(const void *)&norm_kernel<T, 1, 1>, 256, 4};
-    if (c <= 2) return {(const void *)&norm_kernel<T, 1, 2>, 256, 4};
-    if (c <= 4) return {(const void *)&norm_kernel<T, 4, 1>, 256, 1};
-    if (c <= 8) return {(const void *)&norm_kernel<T, 4, 2>, 256, 1};
-    if (c <= 16) return {(const void *)&norm_kernel<T, 4, 4>, 256, 1};
-    if (c <= 32) return {(const void *)&norm_kernel<T, 16, 2>, 1024, 1};
-    return {(const void *)&norm_kernel<T, 16, 4>, 1024, 1};
+    if (cols <= 512) return {(const void *)&norm_kernel<T, 1, 1, kWhole>, 256, 4};
+    if (cols <= 1024) return {(const void *)&norm_kernel<T, 1, 2, kWhole>, 256, 4};
+    if (cols <= 2048) return {(const void *)&norm_kernel<T, 4, 1, kWhole>, 256, 1};
+    if (cols <= 4096) return {(const void *)&norm_kernel<T, 4, 2, kWhole>, 256, 1};
+    if (cols <= 8192) return {(const void *)&norm_kernel<T, 4, 4, kWhole>, 256, 1};
+    if (cols <= 16384) return {(const void *)&norm_kernel<T, 16, 2, kWhole>, 1024, 1};
+    if (cols <= 32768) return {(const void *)&norm_kernel<T, 16, 4, kWhole>, 1024, 1};
+    return {(const void *)&norm_kernel<T, 16, 8, kWhole>, 1024, 1};
 }
-template <typename T>
+template <typename T, bool kWhole>
 Pick pick_grad(int64_t cols) {
-    const int64_t c = ceil_div(cols / 8, kWave);
-    if (c <= 4) return {(const void *)&norm_grad_kernel<T, 4, 1>, 256, 1};
-    if (c <= 8) return {(const void *)&norm_grad_kernel<T, 4, 2>, 256, 1};
-    if (c <= 16) return {(const void *)&norm_grad_kernel<T, 4, 4>, 256, 1};
-    if (c <= 32) return {(const void *)&norm_grad_kernel<T, 16, 2>, 1024, 1};
-    return {(const void *)&norm_grad_kernel<T, 16, 4>, 1024, 1};
+    if (cols <= 512) return {(const void *)&norm_grad_kernel<T, 16, 1, 1, kWhole>, 1024, 16};
+    if (cols <= 1024) return {(const void *)&norm_grad_kernel<T, 8, 2, 1, kWhole>, 1024, 8};
+    if (cols <= 2048) return {(const void *)&norm_grad_kernel<T, 4, 4, 1, kWhole>, 1024, 4};
+    if (cols <= 4096) return {(const void *)&norm_grad_kernel<T, 2, 8, 1, kWhole>, 1024, 2};
+    if (cols <= 8192) return {(const void *)&norm_grad_kernel<T, 1, 16, 1, kWhole>, 1024, 1};
+    return {(const void *)&norm_grad_kernel<T, 1, 16, 2, kWhole>, 1024, 1};
 }
-bool whole_chunks(int64_t cols) { return cols % 8 == 0 && cols <= kWidest; }
+Pick pick_norm(int64_t cols, int dtype) {
+    const bool whole = cols % 8 == 0;
+    if (dtype == FP4Q_OUT_F32) return whole ? pick_norm<float, true>(cols) : pick_norm<float, false>(cols);
+    return whole ? pick_norm<bf16, true>(cols) : pick_norm<bf16, false>(cols);
+}
+Pick pick_grad(int64_t cols, int dtype) {
+    const bool whole = cols % 8 == 0;
+    if (dtype == FP4Q_OUT_F32) return whole ? pick_grad<float, true>(cols) : pick_grad<float, false>(cols);
+    return whole ? pick_grad<bf16, true>(cols) : pick_grad<bf16, false>(cols);
+}
 
-// Parts of dw: as many workgroups as the card holds at once, at most a row each.
+// Parts of dw: a workgroup on each CU, at most as many as their rows need.
 int64_t grad_parts(int64_t rows, int64_t cols) {
-    const int64_t most = whole_chunks(cols) ? 1024 : 64;
-    return rows < most ? rows : most;
+    const int64_t each = cols <= kWidestGrad ? pick_grad(cols, FP4Q_OUT_F32).rows : kAnyWaves;
+    const int64_t need = ceil_div(rows, each);
+    return need < 256 ? need : 256;
 }
 
 }  // namespace
@@ -407,12 +457,12 @@ int fp4q_rmsnorm(const void *x, const void *residual, const void *weight, float 
     if (clash(outs, 5, ins, 3)) return FP4Q_ERR_ARG;
     NormArgs a = {x, residual, weight, h, y, codes, scales, rstd, code_pitch, eps, (int)rows, (int)cols};
     void *args[] = {&a};
-    if (!whole_chunks(cols))
+    if (cols > kWidestNorm)
         return launch(dtype == FP4Q_OUT_F32 ? (const void *)&norm_any_kernel<float>
                                             : (const void *)&norm_any_kernel<bf16>,
                       dim3((unsigned)rows), kAnyWaves * kWave, args, stream);
-    const Pick p = dtype == FP4Q_OUT_F32 ? pick_norm<float>(cols) : pick_norm<bf16>(cols);
-    return launch(p.fn, dim3((unsigned)ceil_div(rows, p.rows_per_wg)), p.threads, args, stream);
+    const Pick p = pick_norm(cols, dtype);
+    return launch(p.fn, dim3((unsigned)ceil_div(rows, p.rows)), p.threads, args, stream);
 }
 
 int fp4q_rmsnorm_backward_workspace(int64_t rows, int64_t cols, size_t *bytes) {
@@ -443,8 +493,8 @@ int fp4q_rmsnorm_backward(const void *dy, const void *h, const void *weight, con
     void *args[] = {&a};
     const bool f32 = dtype == FP4Q_OUT_F32;
     int st = FP4Q_OK;
-    if (rows > 0 && whole_chunks(cols)) {
-        const Pick p = f32 ? pick_grad<float>(cols) : pick_grad<bf16>(cols);
+    if (rows > 0 && cols <= kWidestGrad) {
+        const Pick p = pick_grad(cols, dtype);
         st = launch(p.fn, dim3((unsigned)parts), p.threads, args, stream);
     } else if (rows > 0) {
         st = launch(f32 ? (const void *)&norm_grad_any_kernel<float> : (const void *)&norm_grad_any_kernel<bf16>,
@@ -458,8 +508,8 @@ int fp4q_rmsnorm_backward(const void *dy, const void *h, const void *weight, con
     int c = (int)cols;
     const float *partial = a.partial;
     void *sum_args[] = {&partial, &parts, &c, &dweight};
-    return launch((const void *)&weight_grad_kernel, dim3((unsigned)ceil_div(cols, kSliceCols)),
-                  kSlices * kSliceCols, sum_args, stream);
+    return launch((const void *)&weight_grad_kernel, dim3((unsigned)ceil_div(cols, kSumCols)),
+                  kSlices * kSumLanes, sum_args, stream);
 }
 
 }  // extern "C"

@@ -22,30 +22,9 @@ struct QuantArgs {
     int rows, cols, row_tiles, col_tiles;
 };
 
-template <typename T, bool kVec>
-__device__ __forceinline__ void load_eight(const T *p, int left, float (&v)[8]) {
-    if (kVec) {
-        Eight<T> e;
-        if (left > 0) e.load(p); else e.zero();
-        e.get(v);
-    } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = j < left ? to_float(p[j]) : 0.0f;
-    }
-}
-
-// The first min(left, 8) bytes of w; p is 8-byte aligned.
-__device__ __forceinline__ void store_bytes8(uint8_t *p, int left, u32x2 w) {
-    if (left >= 8) {
-        *reinterpret_cast<u32x2 *>(p) = w;
-    } else {
-        for (int j = 0; j < left; ++j) p[j] = (uint8_t)(w[j >> 2] >> (8 * (j & 3)));
-    }
-}
-
 // Thread t holds rows 8 (t / 16) + i and columns 8 (t % 16) + j of the tile: a
 // row's 128 columns are one DPP row of 16 lanes.
-template <typename T, int kFmt, bool kTiles, bool kVec>
+template <typename T, int kFmt, bool kTiles, bool kWhole>
 __global__ __launch_bounds__(kThreads) void quant_kernel(QuantArgs a) {
     __shared__ unsigned top_lds[kWaves][kGroup];
     __shared__ u32x4 turn[kGroup * kGroup / 16];
@@ -55,10 +34,13 @@ __global__ __launch_bounds__(kThreads) void quant_kernel(QuantArgs a) {
     const int r0 = tr * kGroup + 8 * down, c0 = tc * kGroup + 8 * across;
     const T *x = static_cast<const T *>(a.x) + (int64_t)r0 * a.cols + c0;
 
+    Eight<T> in[8];
     float v[8][8];
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-        load_eight<T, kVec>(x + (int64_t)i * a.cols, r0 + i < a.rows ? a.cols - c0 : 0, v[i]);
+        in[i].template load<kWhole>(x + (int64_t)i * a.cols, r0 + i < a.rows ? a.cols - c0 : 0);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) in[i].get(v[i]);
 
     Scale tile;
     if (kTiles) {
@@ -154,14 +136,14 @@ __global__ __launch_bounds__(kThreads) void quant_kernel(QuantArgs a) {
 }
 
 template <typename T, int kFmt, bool kTiles>
-const void *pick(bool vec) {
-    return vec ? (const void *)&quant_kernel<T, kFmt, kTiles, true>
+const void *pick(bool whole) {
+    return whole ? (const void *)&quant_kernel<T, kFmt, kTiles, true>
                : (const void *)&quant_kernel<T, kFmt, kTiles, false>;
 }
 template <typename T>
-const void *pick(int fmt, bool tiles, bool vec) {
-    if (fmt == FP4Q_E4M3) return tiles ? pick<T, FP4Q_E4M3, true>(vec) : pick<T, FP4Q_E4M3, false>(vec);
-    return tiles ? pick<T, FP4Q_E5M2, true>(vec) : pick<T, FP4Q_E5M2, false>(vec);
+const void *pick(int fmt, bool tiles, bool whole) {
+    if (fmt == FP4Q_E4M3) return tiles ? pick<T, FP4Q_E4M3, true>(whole) : pick<T, FP4Q_E4M3, false>(whole);
+    return tiles ? pick<T, FP4Q_E5M2, true>(whole) : pick<T, FP4Q_E5M2, false>(whole);
 }
 
 }  // namespace
@@ -193,7 +175,7 @@ extern "C" int fp4q_quantize8(const void *x, int64_t rows, int64_t cols, int dty
     QuantArgs a = {x, codes, codes_t, scales, scales_t, code_pitch, code_t_pitch,
                    (int)rows, (int)cols, (int)row_tiles, (int)col_tiles};
     void *args[] = {&a};
-    const bool vec = cols % 8 == 0;
-    const void *fn = dtype == FP4Q_OUT_F32 ? pick<float>(format, tiles, vec) : pick<bf16>(format, tiles, vec);
+    const bool whole = cols % 8 == 0;
+    const void *fn = dtype == FP4Q_OUT_F32 ? pick<float>(format, tiles, whole) : pick<bf16>(format, tiles, whole);
     return launch(fn, dim3((unsigned)(row_tiles * col_tiles)), kThreads, args, stream);
 }
