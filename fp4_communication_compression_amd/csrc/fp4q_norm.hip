@@ -189,8 +189,8 @@ struct GradArgs {
     const void *dy, *h, *weight, *dh;
     const float *rstd;
     void *dx;
-    float *partial;  // [workgroups x cols]
-    int rows, cols;
+    float *partial;  // [workgroups x partial_pitch]
+    int rows, cols, partial_pitch;
 };
 
 // kTeams teams of kWaves wavefronts, a row each at a time; the rows of a workgroup's teams
@@ -296,13 +296,13 @@ __global__ __launch_bounds__(kTeams * kWaves * kWave) void norm_grad_kernel(Grad
                 for (int i = 0; i < 4; ++i) dw[k / 2][4 * (k % 2) + i] += v[i];
             }
     }
-    float *to = a.partial + (int64_t)blockIdx.x * a.cols;
+    float *to = a.partial + (int64_t)blockIdx.x * a.partial_pitch;
 #pragma unroll
     for (int c = 0; c < kChunks; ++c) {
         const int at = first + c * kStep;
         Eight<float> o;
         o.set(dw[c]);
-        o.template store<kWhole>(to + at, a.cols - at);
+        o.template store<kWhole>(to + at, a.cols - at);  // (16-byte aligned in either case)
     }
 }
 
@@ -346,15 +346,15 @@ __global__ __launch_bounds__(kAnyWaves * kWave) void weight_grad_any_kernel(Grad
     if (wave == 0 && k < a.cols) {
 #pragma unroll
         for (int i = 1; i < kAnyWaves; ++i) sum += lds[i][lane];
-        a.partial[(int64_t)blockIdx.y * a.cols + k] = sum;
+        a.partial[(int64_t)blockIdx.y * a.partial_pitch + k] = sum;
     }
 }
 
 // dw = sum of the parts: kSlices slices of them (part p in slice p % kSlices), four columns
 // a thread, then the slices in their order.  A thread's loads do not wait for each other.
 constexpr int kSlices = 32, kSumLanes = 16, kSumCols = 4 * kSumLanes;
-__global__ __launch_bounds__(kSlices * kSumLanes) void weight_grad_kernel(const float *partial, int parts, int cols,
-                                                                          float *dweight) {
+__global__ __launch_bounds__(kSlices * kSumLanes) void weight_grad_kernel(const float *partial, int parts, int pitch,
+                                                                          int cols, float *dweight) {
     __shared__ float lds[kSlices][kSumCols];
     const int lane = threadIdx.x % kSumLanes, slice = threadIdx.x / kSumLanes;
     const int k = (int)blockIdx.x * kSumCols + 4 * lane;
@@ -362,15 +362,13 @@ __global__ __launch_bounds__(kSlices * kSumLanes) void weight_grad_kernel(const 
     if (k + 4 <= cols) {
 #pragma unroll 8
         for (int p = slice; p < parts; p += kSlices) {
-            const u32x4 v = *reinterpret_cast<const Loose<float>::Vec *>(partial + (int64_t)p * cols + k);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) sum[i] += __uint_as_float(v[i]);
+            sum += *reinterpret_cast<const f32x4 *>(partial + (int64_t)p * pitch + k);
         }
     } else {
         for (int p = slice; p < parts; p += kSlices)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                if (k + i < cols) sum[i] += partial[(int64_t)p * cols + k + i];
+                if (k + i < cols) sum[i] += partial[(int64_t)p * pitch + k + i];
     }
     *reinterpret_cast<f32x4 *>(&lds[slice][4 * lane]) = sum;
     __syncthreads();
@@ -422,6 +420,8 @@ Pick pick_grad(int64_t cols, int dtype) {
     return whole ? pick_grad<bf16, true>(cols) : pick_grad<bf16, false>(cols);
 }
 
+int64_t partial_pitch(int64_t cols) { return ceil_div(cols, 4) * 4; }
+
 // Parts of dw: a workgroup on each CU, at most as many as their rows need.
 int64_t grad_parts(int64_t rows, int64_t cols) {
     const int64_t each = cols <= kWidestGrad ? pick_grad(cols, FP4Q_OUT_F32).rows : kAnyWaves;
@@ -468,7 +468,7 @@ int fp4q_rmsnorm(const void *x, const void *residual, const void *weight, float 
 int fp4q_rmsnorm_backward_workspace(int64_t rows, int64_t cols, size_t *bytes) {
     if (bad_dims(rows, cols)) return FP4Q_ERR_SHAPE;
     if (!bytes) return FP4Q_ERR_NULL;
-    *bytes = (size_t)(grad_parts(rows, cols) * cols * 4);
+    *bytes = (size_t)(grad_parts(rows, cols) * partial_pitch(cols) * 4);
     return FP4Q_OK;
 }
 
@@ -483,13 +483,15 @@ int fp4q_rmsnorm_backward(const void *dy, const void *h, const void *weight, con
     for (const void *p : {dy, h, weight, dh, (const void *)dx, (const void *)workspace})
         if (!aligned(p, 16)) return FP4Q_ERR_ALIGN;
     int parts = (int)grad_parts(rows, cols);
-    if (workspace_bytes < (size_t)parts * cols * 4) return FP4Q_ERR_SHAPE;
+    int pitch = (int)partial_pitch(cols);
+    const int64_t need = (int64_t)parts * pitch * 4;
+    if (workspace_bytes < (size_t)need) return FP4Q_ERR_SHAPE;
     const int64_t bytes = rows * cols * esize(dtype);
-    const Range outs[] = {rng(dx, bytes), rng(dweight, 4 * cols), rng(workspace, (int64_t)parts * cols * 4)};
+    const Range outs[] = {rng(dx, bytes), rng(dweight, 4 * cols), rng(workspace, need)};
     const Range ins[] = {rng(dy, bytes), rng(h, bytes), rng(dh, bytes), rng(weight, cols * esize(dtype)),
                          rng(rstd, 4 * rows)};
     if (clash(outs, 3, ins, 5)) return FP4Q_ERR_ARG;
-    GradArgs a = {dy, h, weight, dh, rstd, dx, static_cast<float *>(workspace), (int)rows, (int)cols};
+    GradArgs a = {dy, h, weight, dh, rstd, dx, static_cast<float *>(workspace), (int)rows, (int)cols, pitch};
     void *args[] = {&a};
     const bool f32 = dtype == FP4Q_OUT_F32;
     int st = FP4Q_OK;
@@ -507,7 +509,7 @@ int fp4q_rmsnorm_backward(const void *dy, const void *h, const void *weight, con
     if (st != FP4Q_OK) return st;
     int c = (int)cols;
     const float *partial = a.partial;
-    void *sum_args[] = {&partial, &parts, &c, &dweight};
+    void *sum_args[] = {&partial, &parts, &pitch, &c, &dweight};
     return launch((const void *)&weight_grad_kernel, dim3((unsigned)ceil_div(cols, kSumCols)),
                   kSlices * kSumLanes, sum_args, stream);
 }

@@ -17,7 +17,7 @@ from typing import NamedTuple, Optional
 
 import torch
 
-from . import FP4Q_ERR_SHAPE, FP4Q_OUT_BF16, FP4Q_OUT_F32, Fp4qError, _check, _empty, _stream
+from . import FP4Q_ERR_SHAPE, FP4Q_OUT_BF16, FP4Q_OUT_F32, Fp4qError, _check, _stream
 from . import lib as _base_lib
 
 FP4Q_GROUP8 = 128
@@ -110,10 +110,19 @@ def _typed(t, name):
     return code, rows, cols
 
 
-def _codes_out(rows, cols, dtype, device, stream):
+def _new(like, shape, dtype, stream):
+    """An uninitialised output on the GPU of `like`, allocated for the stream that the
+    kernel will run on (so that its memory goes to no other work meanwhile)."""
+    if stream is None:
+        return like.new_empty(shape, dtype=dtype)
+    with torch.cuda.stream(stream):
+        return like.new_empty(shape, dtype=dtype)
+
+
+def _codes_out(like, rows, cols, dtype, stream):
     """Uninitialised codes [rows, cols] whose rows begin at multiples of 16 bytes."""
     pitch = (cols + 15) // 16 * 16
-    t = _empty((rows, pitch), dtype, device, stream)
+    t = _new(like, (rows, pitch), dtype, stream)
     return t if pitch == cols else t[:, :cols]
 
 
@@ -176,13 +185,13 @@ def fp4q_rmsnorm(x, weight, eps: float, residual=None, h=None, want_y: bool = Tr
         raise ValueError("fp4q: ask for y, codes or both")
     gpu = _gpu(x, weight, residual, given)
     if residual is not None and h is None:
-        h = _empty((rows, cols), kind, gpu, stream)
-    y = _empty((rows, cols), kind, gpu, stream) if want_y else None
+        h = _new(x, (rows, cols), kind, stream)
+    y = _new(x, (rows, cols), kind, stream) if want_y else None
     codes = scales = None
     if want_codes:
-        codes = _codes_out(rows, cols, torch.float8_e4m3fn, gpu, stream)
-        scales = _empty((_groups(cols), rows), torch.float32, gpu, stream)
-    rstd = _empty((rows,), torch.float32, gpu, stream) if want_rstd else None
+        codes = _codes_out(x, rows, cols, torch.float8_e4m3fn, stream)
+        scales = _new(x, (_groups(cols), rows), torch.float32, stream)
+    rstd = _new(x, (rows,), torch.float32, stream) if want_rstd else None
     _check(_lib().fp4q_rmsnorm(_at(x), _at(residual), _at(weight), eps, rows, cols, dtype, _at(h), _at(y),
                                _at(codes), (cols + 15) // 16 * 16, _at(scales), _at(rstd),
                                _launch_stream(stream, gpu)))
@@ -201,9 +210,9 @@ def fp4q_rmsnorm_backward(dy, h, weight, rstd, dh=None, stream=None):
         _like(dh, "dh", dy.shape, dy.dtype)
     gpu = _gpu(dy, h, weight, rstd, dh)
     need = _workspace("fp4q_rmsnorm_backward_workspace", rows, cols)
-    dx = _empty((rows, cols), dy.dtype, gpu, stream)
-    dweight = _empty((cols,), torch.float32, gpu, stream)
-    space = _empty((need,), torch.uint8, gpu, stream)
+    dx = _new(dy, (rows, cols), dy.dtype, stream)
+    dweight = _new(dy, (cols,), torch.float32, stream)
+    space = _new(dy, (need,), torch.uint8, stream)
     _check(_lib().fp4q_rmsnorm_backward(_at(dy), _at(h), _at(weight), _at(rstd), _at(dh), rows, cols, dtype,
                                         _at(dx), _at(dweight), _at(space), need, _launch_stream(stream, gpu)))
     return dx, dweight
@@ -232,11 +241,11 @@ def fp4q_quantize8(x, dtype=torch.float8_e4m3fn, tiles: bool = False, straight: 
     codes = scales = codes_t = scales_t = None
     gr, gc = _groups(rows), _groups(cols)
     if straight:
-        codes = _codes_out(rows, cols, dtype, gpu, stream)
-        scales = _empty((gc, gr if tiles else rows), torch.float32, gpu, stream)
+        codes = _codes_out(x, rows, cols, dtype, stream)
+        scales = _new(x, (gc, gr if tiles else rows), torch.float32, stream)
     if transposed:
-        codes_t = _codes_out(cols, rows, dtype, gpu, stream)
-        scales_t = _empty((gr, gc if tiles else cols), torch.float32, gpu, stream)
+        codes_t = _codes_out(x, cols, rows, dtype, stream)
+        scales_t = _new(x, (gr, gc if tiles else cols), torch.float32, stream)
     _check(_lib().fp4q_quantize8(_at(x), rows, cols, kind, fmt, _at(codes), (cols + 15) // 16 * 16, _at(scales),
                                  _at(codes_t), (rows + 15) // 16 * 16, _at(scales_t),
                                  FP4Q_FLAG_TILES if tiles else 0, _launch_stream(stream, gpu)))
@@ -271,8 +280,8 @@ def fp4q_gemm8(a, a_scales, b, b_scales, out=None, out_dtype=None, accumulate: b
     flags = (FP4Q_FLAG_TILES if tiles else 0) | (FP4Q_FLAG_ACCUMULATE if accumulate else 0)
     need = _workspace("fp4q_gemm8_workspace", M, N, K, code, flags)
     if out is None:
-        out = _empty((M, N), dtype, gpu, stream)
-    space = _empty((need,), torch.uint8, gpu, stream) if need else None
+        out = _new(a_scales, (M, N), dtype, stream)
+    space = _new(a_scales, (need,), torch.uint8, stream) if need else None
     _check(_lib().fp4q_gemm8(_at(a), a_pitch, fa, _at(a_scales), _at(b), b_pitch, fb, _at(b_scales), M, N, K,
                              _at(out), code, flags, _at(space), need, _launch_stream(stream, gpu)))
     return out

@@ -172,7 +172,7 @@ def norm_grad(dy=G, h=2 * G, weight=3 * G, rstd=4 * G, dh=5 * G, rows=4, cols=25
 @pytest.mark.parametrize("change,want", [
     ({"rows": -1}, SHAPE), ({"cols": 0}, SHAPE), ({"dtype": -1}, ARG), ({"dy": None}, NULL), ({"h": None}, NULL),
     ({"weight": None}, NULL), ({"rstd": None}, NULL), ({"dx": None}, NULL), ({"dw": None}, NULL),
-    ({"rows": 0, "dw": None}, NULL), ({"space": None}, NULL), ({"size": 4 * 256 * 4 - 1}, SHAPE),
+    ({"rows": 0, "dw": None}, NULL), ({"space": None}, NULL), ({"size": 256 * 4 - 1}, SHAPE),
     ({"dx": 6 * G + 4}, ALIGN), ({"dw": 7 * G + 2}, ALIGN), ({"space": 8 * G + 8}, ALIGN), ({"dx": G}, ARG),
     ({"dx": 5 * G}, ARG), ({"dw": 3 * G}, ARG), ({"space": 6 * G + 64}, ARG)])
 def test_rmsnorm_backward_refuses(change, want):
