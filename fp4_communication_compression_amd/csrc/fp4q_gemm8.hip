@@ -58,28 +58,31 @@ struct GemmArgs {
     float *partial;
 };
 
-// 32 codes of one row (half a block's 64 for every 16 lanes, in the order that both
-// operands share) as the matrix core takes them.
+// 32 codes of a row as loaded (of a block's 128, in an order that both operands share) ...
+struct Raw {
+    u32x4 low, high;
+};
+// ... and as the matrix core takes them.
 template <int kFmt, bool kPrecise>
 struct Frag;
 template <int kFmt>
 struct Frag<kFmt, false> {
     i32x8 v;
-    __device__ __forceinline__ void set(u32x4 lo, u32x4 hi) {
+    __device__ __forceinline__ void set(const Raw &raw) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            v[i] = (int)lo[i];
-            v[4 + i] = (int)hi[i];
+            v[i] = (int)raw.low[i];
+            v[4 + i] = (int)raw.high[i];
         }
     }
 };
 template <int kFmt>
 struct Frag<kFmt, true> {
     bf16x8 v[4];
-    __device__ __forceinline__ void set(u32x4 lo, u32x4 hi) {
+    __device__ __forceinline__ void set(const Raw &raw) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const unsigned w = i < 4 ? lo[i] : hi[i - 4];
+            const unsigned w = i < 4 ? raw.low[i] : raw.high[i - 4];
             bf16x2 p, q;
             if constexpr (kFmt == FP4Q_E4M3) {
                 p = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, false);
@@ -267,15 +270,11 @@ struct Tile {
         return *reinterpret_cast<const T *>(reinterpret_cast<const char *>(&in) + offset);
     }
     static constexpr int kA = (int)__builtin_offsetof(Stage<S>, a), kB = (int)__builtin_offsetof(Stage<S>, b);
-    __device__ __forceinline__ Frag<kFmtA, kPrecise> frag_a(const Stage<S> &in, int i) {
-        Frag<kFmtA, kPrecise> f;
-        f.set(at<u32x4>(in, low_a + (kA + i * 16 * kGroup)), at<u32x4>(in, high_a + (kA + i * 16 * kGroup)));
-        return f;
+    __device__ __forceinline__ Raw raw_a(const Stage<S> &in, int i) {
+        return {at<u32x4>(in, low_a + (kA + i * 16 * kGroup)), at<u32x4>(in, high_a + (kA + i * 16 * kGroup))};
     }
-    __device__ __forceinline__ Frag<kFmtB, kPrecise> frag_b(const Stage<S> &in, int j) {
-        Frag<kFmtB, kPrecise> f;
-        f.set(at<u32x4>(in, low_b + (kB + j * 16 * kGroup)), at<u32x4>(in, high_b + (kB + j * 16 * kGroup)));
-        return f;
+    __device__ __forceinline__ Raw raw_b(const Stage<S> &in, int j) {
+        return {at<u32x4>(in, low_b + (kB + j * 16 * kGroup)), at<u32x4>(in, high_b + (kB + j * 16 * kGroup))};
     }
     __device__ __forceinline__ float scale_a(const Stage<S> &in, int i) {
         return at<float>(in, 4 * (wm + row16) + 64 * i);
@@ -283,13 +282,12 @@ struct Tile {
 
     // What a block's multiplication begins with, read during the one before it.
     struct Head {
-        Frag<kFmtB, kPrecise> b[S::kTilesN];
-        Frag<kFmtA, kPrecise> a;
+        Raw b[S::kTilesN], a;
         float sa, sb;
     };
     __device__ __forceinline__ void read_head(const Stage<S> &in, Head &h, int item) {
         if (item == 0) {
-            h.a = frag_a(in, 0);
+            h.a = raw_a(in, 0);
             h.sa = scale_a(in, 0);
             h.sb = 1.0f;
             if constexpr (kTiles) {
@@ -297,7 +295,7 @@ struct Tile {
                 h.sb = at<float>(in, 4 * (in.kScalesA + wn / kGroup));
             }
         } else {
-            h.b[item - 1] = frag_b(in, item - 1);
+            h.b[item - 1] = raw_b(in, item - 1);
         }
     }
 
@@ -322,13 +320,15 @@ struct Tile {
     __device__ __forceinline__ void step(Stage<S> &cur, Stage<S> &nxt, Head &h, Head &n, int kb, int end, bool ragged) {
         constexpr int kLag = 3, kTilesM = S::kTilesM, kTilesN = S::kTilesN;
         constexpr int kCount = kTilesM * kTilesN;
-        Frag<kFmtA, kPrecise> fa[kTilesM];
+        Raw ra[kTilesM];
+        Frag<kFmtA, kPrecise> fa[2];
+        Frag<kFmtB, kPrecise> fb[kTilesN];
         float sa[kTilesM];
         f32x4 sb[kTilesN], d[kLag + 1];
-        fa[0] = h.a;
+        ra[0] = h.a;
         sa[0] = h.sa;
 #pragma unroll
-        for (int j = kHeadB; j < kTilesN; ++j) h.b[j] = frag_b(cur, j);
+        for (int j = kHeadB; j < kTilesN; ++j) h.b[j] = raw_b(cur, j);
         if constexpr (!kTiles) {
 #pragma unroll
             for (int j = 0; j < kTilesN; ++j)
@@ -339,7 +339,7 @@ struct Tile {
             if constexpr (j == 0 && i < kMeet) {
                 constexpr int from = i ? rows_read(i - 1) : 1, count = rows_read(i) - from;
                 static_for<count>([&](auto k) FP4Q_INLINE {
-                    fa[from + k.value] = frag_a(cur, from + k.value);
+                    ra[from + k.value] = raw_a(cur, from + k.value);
                     sa[from + k.value] = scale_a(cur, from + k.value);
                 });
             }
@@ -357,8 +357,15 @@ struct Tile {
                 constexpr int from = i > kMeet ? head_read(i - 1) : 0, count = head_read(i) - from;
                 static_for<count>([&](auto k) FP4Q_INLINE { read_head(nxt, n, from + k.value); });
             }
-            if constexpr (t < kCount) d[t % (kLag + 1)] = block_product(h.b[j], fa[i]);
+            if constexpr (t < kCount) {
+                // fragments are made where their first product needs them, and the next row's
+                // while the matrix core works on this one's
+                if constexpr (t == 0) fa[0].set(ra[0]);
+                if constexpr (i == 0) fb[j].set(h.b[j]);
+                d[t % (kLag + 1)] = block_product(fb[j], fa[i & 1]);
+            }
             __builtin_amdgcn_sched_barrier(0);  // the matrix core first
+            if constexpr (j == kTilesN - 1 && i + 1 < kTilesM) fa[(i + 1) & 1].set(ra[i + 1]);
             if constexpr (t >= kLag) {
                 constexpr int ui = (t - kLag) / kTilesN, uj = (t - kLag) % kTilesN;
                 if constexpr (kTiles && uj == 0) sa[ui] *= h.sb;
@@ -601,11 +608,11 @@ __global__ __launch_bounds__(S::kThreads) void strip_kernel(GemmArgs p) {
 #pragma unroll
             for (int j = 0; j < S::kNT; ++j) {
                 Frag<kFmtB, kPrecise> first;
-                first.set(fb[u][j][0], fb[u][j][1]);
+                first.set({fb[u][j][0], fb[u][j][1]});
 #pragma unroll
                 for (int i = 0; i < S::kMT; ++i) {
                     Frag<kFmtA, kPrecise> second;
-                    second.set(fa[u][i][0], fa[u][i][1]);
+                    second.set({fa[u][i][0], fa[u][i][1]});
                     const f32x4 d = block_product(first, second);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) acc[i][j][e] = fmaf(d[e], sa[u][i] * sb[u][j][e], acc[i][j][e]);
