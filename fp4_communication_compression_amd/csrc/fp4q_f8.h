@@ -235,7 +235,9 @@ inline bool bad_dims(int64_t rows, int64_t cols) {
 }
 inline int esize(int dtype) { return dtype == FP4Q_OUT_F32 ? 4 : 2; }
 
+// A launch's size is counted in threads, in 32 bits.
 inline int launch(const void *fn, dim3 grid, int threads, void **args, void *stream) {
+    if ((uint64_t)grid.x * (uint64_t)threads > 0xFFFFFFFFu) return FP4Q_ERR_SHAPE;
     const hipError_t e = hipLaunchKernel(fn, grid, dim3((unsigned)threads), args, 0, (hipStream_t)stream);
     return e == hipSuccess ? FP4Q_OK : FP4Q_ERR_LAUNCH;
 }

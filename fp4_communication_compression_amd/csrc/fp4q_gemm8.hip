@@ -151,13 +151,14 @@ __device__ __forceinline__ void load_to_lds(void *to, const void *from, int byte
                               (unsigned)__builtin_amdgcn_readfirstlane((int)((base >> 32) & 0xFFFF)),
                               (unsigned)__builtin_amdgcn_readfirstlane(max(bytes, 0)), 0x00020000u};
     const int at = __builtin_amdgcn_readfirstlane((int)(unsigned)(uintptr_t)(lds_void *)to);
-    // the wait states between scalar writes and the load that reads them
+    // M0 holds the address in LDS; the compiler keeps nothing in it from one instruction to
+    // the next.  Then the wait states between scalar writes and the load that reads them.
     if constexpr (kBytes == 16)
         asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
-                     : : "s"(at), "v"(offset), "s"(descriptor) : "memory", "m0");
+                     : : "s"(at), "v"(offset), "s"(descriptor) : "memory");
     else
         asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dword %1, %2, 0 offen lds"
-                     : : "s"(at), "v"(offset), "s"(descriptor) : "memory", "m0");
+                     : : "s"(at), "v"(offset), "s"(descriptor) : "memory");
 }
 
 // A meeting of the workgroup's wavefronts, each with at most kLeft of its loads into LDS

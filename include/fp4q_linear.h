@@ -34,7 +34,8 @@
  * alignment, workspace size (FP4Q_ERR_SHAPE) and overlap of an output with an
  * input or another output (FP4Q_ERR_ARG)), FP4Q_ERR_LAUNCH for a failed launch.
  * Tensors, codes and workspaces are aligned to 16 bytes, scales, rstd, dweight
- * to 4.  Results do not depend on timing: no atomics, every sum in a fixed order.
+ * to 4.  A size that would need more than 2^32 - 1 threads returns FP4Q_ERR_SHAPE.
+ * Results do not depend on timing: no atomics, every sum in a fixed order.
  * Element types are FP4Q_OUT_F32 and FP4Q_OUT_BF16.
  */
 #ifndef FP4Q_LINEAR_H
@@ -94,7 +95,8 @@ int fp4q_rmsnorm_backward(const void *dy, const void *h, const void *weight, con
  *                      pitch code_t_pitch): its blocks are 128 neighbours in a
  *                      column of x; with FP4Q_FLAG_TILES the same tiles, so
  *                      that codes_t holds the same codes
- * Either pair may be NULL, not both.  rows >= 0, 1 <= cols; rows, cols < 2^28. */
+ * Either pair may be NULL, not both.  rows >= 0, 1 <= cols; rows, cols < 2^28,
+ * fewer than 2^31 tiles of 128 x 128. */
 int fp4q_quantize8(const void *x, int64_t rows, int64_t cols, int dtype, int format, uint8_t *codes,
                    int64_t code_pitch, float *scales, uint8_t *codes_t, int64_t code_t_pitch,
                    float *scales_t, uint32_t flags, void *stream);

@@ -215,6 +215,16 @@ def test_gemm_refuses(change, want):
     assert gemm(**change) == want
 
 
+@fake_addresses
+def test_launches_past_32_bits_are_refused():
+    """More threads than a launch can count, found before any HIP call."""
+    far = 1 << 50
+    assert norm(x=far, residual=None, h=None, weight=2 * far, y=3 * far, codes=None, scales=None, rstd=None,
+                rows=1 << 27, cols=20000) == SHAPE
+    assert gemm(a=far, sa=2 * far, b=3 * far, sb=4 * far, out=5 * far, m=1, n=(1 << 28) - 1, k=128, a_pitch=128,
+                b_pitch=128, space=None, size=0) == SHAPE
+
+
 def test_workspace_sizes():
     L, size = library(), ctypes.c_size_t()
     assert L.fp4q_rmsnorm_backward_workspace(4, 0, ctypes.byref(size)) == SHAPE

@@ -381,3 +381,88 @@ def test_streams_and_graphs(fp4q, rows):
         torch.cuda.synchronize()
         eager = layer(fp4q, x, res, w, qw)
         assert all(torch.equal(a, b) for a, b in zip(eager, held)), turn
+
+
+# ------------------------------------------------- together, and past 32 bits
+@pytest.mark.parametrize("ranks,tokens,hidden,inner", [(2, 96, 512, 1024), (4, 7, 256, 528), (1, 200, 512, 300)])
+def test_example_layer(fp4q, ranks, tokens, hidden, inner):
+    """The tensor-parallel layer of examples/tp_layer.py against fp32.  An 8-bit operand is off
+    by at most 2^-4 (E4M3) or 2^-3 (E5M2) of a value, which random values average to at most
+    0.04 and 0.08 of a product's norm; the layer chains two products with a square between
+    (twice the first one's error) and as many back.  FP4 adds at most 0.25 a value, 0.15 in
+    the norm, at each of two exchanges."""
+    from examples import tp_layer
+    plain = tp_layer.errors(ranks, tokens, hidden, inner, compress=False)
+    fp4 = tp_layer.errors(ranks, tokens, hidden, inner, compress=True)
+    print(plain, fp4, flush=True)
+    assert max(plain.values()) < 0.2
+    assert max(fp4.values()) < 0.5
+
+
+def test_norm_past_32_bits(fp4q):
+    rows, cols = 140000, 16384
+    x = torch.zeros(rows, cols, dtype=BF16, device=DEV)
+    tail = rand(torch.Generator().manual_seed(0), 5, cols, BF16)
+    x[-5:] = tail.to(DEV)
+    w = torch.ones(cols, dtype=BF16, device=DEV)
+    out = fp4q.fp4q_rmsnorm(x, w, EPS, want_codes=True, want_rstd=True)
+    r, y = ref.norm(tail, w.cpu(), EPS)
+    within(out.y[-5:].cpu(), y, (60 * ref.U + 2.0 ** -8) * y.abs())
+    within(ref.values(down(out.codes[-5:]), out.scales[:, -5:].cpu()), y, 2.0 ** -3.9 * y.abs() + 1e-2)
+    assert bool((out.y[:3] == 0).all()) and bool((out.y[-9:-5] == 0).all())
+    del out
+    dy = torch.zeros_like(x)
+    dy[-5:] = tail.flip(0).to(DEV)
+    rstd = torch.zeros(rows, device=DEV)
+    rstd[-5:] = r.float().to(DEV)
+    dx, dw = fp4q.fp4q_rmsnorm_backward(dy, x, w, rstd)
+    want, off, want_w, off_w = ref.norm_grad(tail.flip(0), tail, w.cpu(), r.float(), None)
+    within(dx[-5:].cpu(), want, off + 2.0 ** -8 * (want.abs() + off))
+    within(dw.cpu(), want_w, off_w)
+    assert bool((dx[-9:-5] == 0).all())
+
+
+def test_quantize_past_32_bits(fp4q):
+    rows, cols = 140000, 16384
+    x = torch.zeros(rows, cols, dtype=BF16, device=DEV)
+    tail = rand(torch.Generator().manual_seed(0), 64, cols, BF16)   # rows 139936 ..: 32 of the last tile, 32 before
+    x[-64:] = tail.to(DEV)
+    q = fp4q.fp4q_quantize8(x, transposed=True)
+    check_codes(q.codes[-64:], q.scales[:, -64:], tail.float(), E4M3, False)
+    part = torch.zeros(cols, 256)                                   # rows 139776 .. 140032, two groups
+    part[:, 160:224] = tail.float().t()
+    want, scales = ref.quantize(part, E4M3, False)
+    assert same(down(q.codes_t[:, 139776:]).float(), want[:, :224])
+    assert same(q.scales_t[1092:].cpu(), scales)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_gemm_past_32_bits(fp4q, dtype):
+    m, n, k = 50000, 45000, 130
+    gen = torch.Generator().manual_seed(0)
+    a, sa, b, sb = make(gen, 300, 300, k, E4M3, E4M3, False)
+    big_a = torch.zeros(m, 144, dtype=torch.uint8, device=DEV).view(E4M3)[:, :k]
+    big_b = torch.zeros(n, 144, dtype=torch.uint8, device=DEV).view(E4M3)[:, :k]
+    big_a.view(torch.uint8)[-300:] = a.view(torch.uint8).to(DEV)
+    big_b.view(torch.uint8)[-300:] = b.view(torch.uint8).to(DEV)
+    scale_a, scale_b = torch.ones(2, m, device=DEV), torch.ones(2, n, device=DEV)
+    scale_a[:, -300:] = sa.to(DEV)
+    scale_b[:, -300:] = sb.to(DEV)
+    out = fp4q.fp4q_gemm8(big_a, scale_a, big_b, scale_b, out_dtype=dtype)
+    got = out[-300:, -300:].cpu()
+    if dtype == F32:
+        within(got, *ref.gemm(a, sa, b, sb))
+    else:
+        check_bf16(got, a, sa, b, sb)
+    assert bool((out[-301] == 0).all()) and bool((out[-300:, -301] == 0).all()) and bool((out[:2] == 0).all())
+
+
+def test_gemm_of_a_long_sum(fp4q):
+    """A contraction of 1.5 million: a tile's rows span 192 MB and more."""
+    k = 1500000
+    gen = torch.Generator().manual_seed(0)
+    a, sa, b, sb = make(gen, 40, 300, k, E4M3, E4M3, True)
+    va, vb = (ref.values(x, s).to(DEV) for x, s in ((a, sa), (b, sb)))
+    want = (va @ vb.t()).cpu()
+    off = (va.abs() @ vb.abs().t()).cpu() * ref.U * (2 * 128 + sa.shape[0] + 8)
+    within(fp4q.fp4q_gemm8(up(a), sa.to(DEV), up(b), sb.to(DEV), out_dtype=F32).cpu(), want, off)
