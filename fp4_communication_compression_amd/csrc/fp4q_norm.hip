@@ -274,7 +274,7 @@ __global__ __launch_bounds__(kTeams * kWaves * kWave) void norm_grad_kernel(Grad
             Eight<T> o;
             o.set(p);
             const int at = first + c * kStep;
-            o.template store<kWhole>(static_cast<T *>(a.dx) + base + at, row < a.rows ? a.cols - at : 0);
+            o.template store<kWhole, false>(static_cast<T *>(a.dx) + base + at, row < a.rows ? a.cols - at : 0);
         }
         if (kAhead) now = next; else load(now, row + stride);
     }
@@ -302,7 +302,7 @@ __global__ __launch_bounds__(kTeams * kWaves * kWave) void norm_grad_kernel(Grad
         const int at = first + c * kStep;
         Eight<float> o;
         o.set(dw[c]);
-        o.template store<kWhole>(to + at, a.cols - at);  // (16-byte aligned in either case)
+        o.template store<kWhole, false>(to + at, a.cols - at);  // (16-byte aligned in either case)
     }
 }
 

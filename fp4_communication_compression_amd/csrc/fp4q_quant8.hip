@@ -125,7 +125,7 @@ __global__ __launch_bounds__(kThreads) void quant_kernel(QuantArgs a) {
             if (col < a.cols && row < a.rows) {
                 uint8_t *p = a.codes_t + (int64_t)col * a.pitch_t + row;
                 if (a.rows - row >= 16) {
-                    *reinterpret_cast<u32x4 *>(p) = w;
+                    __builtin_nontemporal_store(w, reinterpret_cast<u32x4 *>(p));
                 } else {
                     store_bytes8(p, a.rows - row, u32x2{w[0], w[1]});
                     if (a.rows - row > 8) store_bytes8(p + 8, a.rows - row - 8, u32x2{w[2], w[3]});
