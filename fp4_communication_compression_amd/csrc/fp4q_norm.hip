@@ -422,11 +422,12 @@ Pick pick_grad(int64_t cols, int dtype) {
 
 int64_t partial_pitch(int64_t cols) { return ceil_div(cols, 4) * 4; }
 
-// Parts of dw: a workgroup on each CU, at most as many as their rows need.
+// Parts of dw: at most a workgroup on each CU, and no more than make the same number of
+// turns (333 rows in turns of one: 167 workgroups take two turns as 256 do).
 int64_t grad_parts(int64_t rows, int64_t cols) {
     const int64_t each = cols <= kWidestGrad ? pick_grad(cols, FP4Q_OUT_F32).rows : kAnyWaves;
-    const int64_t need = ceil_div(rows, each);
-    return need < 256 ? need : 256;
+    const int64_t need = ceil_div(rows, each), turns = ceil_div(need, 256);
+    return need ? ceil_div(need, turns) : 0;
 }
 
 }  // namespace

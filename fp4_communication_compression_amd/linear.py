@@ -192,9 +192,11 @@ def fp4q_rmsnorm(x, weight, eps: float, residual=None, h=None, want_y: bool = Tr
         codes = _codes_out(x, rows, cols, torch.float8_e4m3fn, stream)
         scales = _new(x, (_groups(cols), rows), torch.float32, stream)
     rstd = _new(x, (rows,), torch.float32, stream) if want_rstd else None
-    _check(_lib().fp4q_rmsnorm(_at(x), _at(residual), _at(weight), eps, rows, cols, dtype, _at(h), _at(y),
-                               _at(codes), (cols + 15) // 16 * 16, _at(scales), _at(rstd),
-                               _launch_stream(stream, gpu)))
+    status = (_bound or _lib()).fp4q_rmsnorm(_at(x), _at(residual), _at(weight), eps, rows, cols, dtype, _at(h), _at(y),
+                                             _at(codes), (cols + 15) // 16 * 16, _at(scales), _at(rstd),
+                                             _launch_stream(stream, gpu))
+    if status:
+        raise Fp4qError(status)
     return RmsNorm(x if residual is None else h, y, codes, scales, rstd)
 
 
@@ -213,8 +215,11 @@ def fp4q_rmsnorm_backward(dy, h, weight, rstd, dh=None, stream=None):
     dx = _new(dy, (rows, cols), dy.dtype, stream)
     dweight = _new(dy, (cols,), torch.float32, stream)
     space = _new(dy, (need,), torch.uint8, stream)
-    _check(_lib().fp4q_rmsnorm_backward(_at(dy), _at(h), _at(weight), _at(rstd), _at(dh), rows, cols, dtype,
-                                        _at(dx), _at(dweight), _at(space), need, _launch_stream(stream, gpu)))
+    status = (_bound or _lib()).fp4q_rmsnorm_backward(_at(dy), _at(h), _at(weight), _at(rstd), _at(dh), rows, cols,
+                                                      dtype, _at(dx), _at(dweight), _at(space), need,
+                                                      _launch_stream(stream, gpu))
+    if status:
+        raise Fp4qError(status)
     return dx, dweight
 
 
@@ -246,9 +251,11 @@ def fp4q_quantize8(x, dtype=torch.float8_e4m3fn, tiles: bool = False, straight: 
     if transposed:
         codes_t = _codes_out(x, cols, rows, dtype, stream)
         scales_t = _new(x, (gr, gc if tiles else cols), torch.float32, stream)
-    _check(_lib().fp4q_quantize8(_at(x), rows, cols, kind, fmt, _at(codes), (cols + 15) // 16 * 16, _at(scales),
-                                 _at(codes_t), (rows + 15) // 16 * 16, _at(scales_t),
-                                 FP4Q_FLAG_TILES if tiles else 0, _launch_stream(stream, gpu)))
+    status = (_bound or _lib()).fp4q_quantize8(_at(x), rows, cols, kind, fmt, _at(codes), (cols + 15) // 16 * 16,
+                                               _at(scales), _at(codes_t), (rows + 15) // 16 * 16, _at(scales_t),
+                                               FP4Q_FLAG_TILES if tiles else 0, _launch_stream(stream, gpu))
+    if status:
+        raise Fp4qError(status)
     return Quantized8(codes, scales, codes_t, scales_t)
 
 
@@ -282,6 +289,8 @@ def fp4q_gemm8(a, a_scales, b, b_scales, out=None, out_dtype=None, accumulate: b
     if out is None:
         out = _new(a_scales, (M, N), dtype, stream)
     space = _new(a_scales, (need,), torch.uint8, stream) if need else None
-    _check(_lib().fp4q_gemm8(_at(a), a_pitch, fa, _at(a_scales), _at(b), b_pitch, fb, _at(b_scales), M, N, K,
-                             _at(out), code, flags, _at(space), need, _launch_stream(stream, gpu)))
+    status = (_bound or _lib()).fp4q_gemm8(_at(a), a_pitch, fa, _at(a_scales), _at(b), b_pitch, fb, _at(b_scales), M, N, K,
+                                           _at(out), code, flags, _at(space), need, _launch_stream(stream, gpu))
+    if status:
+        raise Fp4qError(status)
     return out
