@@ -50,7 +50,7 @@ struct GemmArgs {
     int64_t a_pitch, b_pitch;
     int M, N, K;
     int tiles_m, tiles_n;
-    int out_f32, accumulate;
+    int accumulate;
     // K in `parts` runs of blocks, a workgroup each; with more than one, run s's sums go
     // to partial + s part_size, and join_kernel adds them
     int parts;
@@ -247,6 +247,7 @@ struct Tile {
                        min(count - at, kWave) * 4, 4 * lane);
     }
     static constexpr int kFetched = S::kLoadsA + S::kLoadsB + 1;  // loads of a wavefront and block
+
     // Clears the codes from K on in the last block.
     __device__ __forceinline__ void clear_tail(Stage<S> &in) {
         const int left = p.K % kGroup;
@@ -541,120 +542,89 @@ __device__ __forceinline__ u32x4 load_chunk(const uint8_t *row, int k, int K) {
     return w;
 }
 
-// Few rows of a: the time is that of reading b once.  A workgroup takes 16 kNT rows of
-// b; its wavefronts share K, each taking every kWaves-th block, whole fragments straight
+// Up to 16 rows of a: the time is that of reading b once.  A workgroup takes 16 rows of
+// b; its wavefronts share K, each taking every kStripWaves-th block, whole fragments straight
 // from memory into registers, kAhead blocks' loads at a time.  A load takes 64 neighbouring
 // bytes of each of 16 rows (with a lane's 32 bytes side by side, 16 bytes at every 32, it
 // took a tenth longer).  The parts of the sum are joined through LDS in the wavefronts'
-// order.  4096 x 11008 codes read from HBM take 12.5 us (3.6 TB/s), 32768 x 4096 33 us
-// (4.1 TB/s), for 1 to 16 rows of a.
-template <int kMT_, int kNT_, int kWaves_, int kAhead_>
-struct Strip {
-    static constexpr int kMT = kMT_, kNT = kNT_, kWaves = kWaves_, kAhead = kAhead_;
-    static constexpr int kThreads = kWaves * kWave, kM = 16 * kMT, kN = 16 * kNT;
-};
-template <typename S, int kFmtA, int kFmtB, bool kTiles, bool kPrecise>
-__global__ __launch_bounds__(S::kThreads) void strip_kernel(GemmArgs p) {
-    __shared__ f32x4 part[S::kWaves][S::kMT * S::kNT][kWave];
+// order.  4096 x 11008 codes read from HBM take 13 us (3.5 TB/s), 32768 x 4096 33 us
+// (4.1 TB/s, with two workgroups on a CU: at most 64 registers; 37 us with one), for 1 to
+// 16 rows of a.
+constexpr int kStrip = 16, kStripWaves = 16, kAhead = 4, kStripThreads = kStripWaves * kWave;
+template <int kFmtA, int kFmtB, bool kTiles, bool kPrecise>
+__global__ __launch_bounds__(kStripThreads, kTiles && !kPrecise ? 8 : 4) void strip_kernel(GemmArgs p) {
+    __shared__ f32x4 part[kStripWaves][kWave];
     const int lane = threadIdx.x & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int row16 = lane & 15, quarter = lane >> 4;
-    const int n0 = (int)blockIdx.x * S::kN;  // (one tile in m)
-    const int blocks = (p.K + kGroup - 1) / kGroup;
-    const int cols_sb = kTiles ? (p.N + kGroup - 1) / kGroup : p.N;
-    const uint8_t *a[S::kMT], *b[S::kNT];
-    int m[S::kMT];
-#pragma unroll
-    for (int i = 0; i < S::kMT; ++i) {
-        m[i] = min(i * 16 + row16, p.M - 1);
-        a[i] = p.a + m[i] * p.a_pitch;
-    }
-#pragma unroll
-    for (int j = 0; j < S::kNT; ++j) b[j] = p.b + min(n0 + j * 16 + row16, p.N - 1) * p.b_pitch;
-    f32x4 acc[S::kMT][S::kNT];
-#pragma unroll
-    for (int i = 0; i < S::kMT; ++i)
-#pragma unroll
-        for (int j = 0; j < S::kNT; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+    const int n0 = (int)blockIdx.x * kStrip;  // within one of b's tiles of scales
+    const int blocks = (p.K + kGroup - 1) / kGroup, whole = p.K / kGroup;
+    const int cols = kTiles ? (p.N + kGroup - 1) / kGroup : p.N;
+    // rows past the end repeat the last one
+    const int m = min(row16, p.M - 1);
+    const uint8_t *a = p.a, *b = p.b + n0 * p.b_pitch;
+    const unsigned row_a = m * (unsigned)p.a_pitch, row_b = (min(n0 + row16, p.N - 1) - n0) * (unsigned)p.b_pitch;
+    f32x4 acc = {0, 0, 0, 0};
 
-    auto run = [&](int kb0, auto count_of, auto whole_of) {
+    // kCount blocks from kb0, kStripWaves apart; kWhole: all their codes lie before K
+    auto run = [&](int kb0, auto count_of, auto whole_of) FP4Q_INLINE {
         constexpr int kCount = count_of.value;
-        constexpr bool kWhole = whole_of.value;  // no end of K inside
-        u32x4 fa[kCount][S::kMT][2], fb[kCount][S::kNT][2];
-        float sa[kCount][S::kMT];
-        f32x4 sb[kCount][S::kNT];
+        constexpr bool kWhole = whole_of.value;
+        Raw ra[kCount], rb[kCount];
+        float sa[kCount];
+        f32x4 sb[kCount];
 #pragma unroll
         for (int u = 0; u < kCount; ++u) {
-            const int kb = kb0 + u * S::kWaves, k = kb * kGroup + 16 * quarter;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-#pragma unroll
-                for (int j = 0; j < S::kNT; ++j)
-                    fb[u][j][h] = kWhole ? *reinterpret_cast<const u32x4 *>(b[j] + k + 64 * h)
-                                         : load_chunk(b[j], k + 64 * h, p.K);
-#pragma unroll
-                for (int i = 0; i < S::kMT; ++i)
-                    fa[u][i][h] = kWhole ? *reinterpret_cast<const u32x4 *>(a[i] + k + 64 * h)
-                                         : load_chunk(a[i], k + 64 * h, p.K);
+            const int kb = kb0 + u * kStripWaves, low = kb * kGroup + 16 * quarter;
+            if constexpr (kWhole) {
+                rb[u] = {*reinterpret_cast<const u32x4 *>(b + (row_b + low)),
+                         *reinterpret_cast<const u32x4 *>(b + (row_b + low) + 64)};
+                ra[u] = {*reinterpret_cast<const u32x4 *>(a + (row_a + low)),
+                         *reinterpret_cast<const u32x4 *>(a + (row_a + low) + 64)};
+            } else {
+                rb[u] = {load_chunk(b + row_b, low, p.K), load_chunk(b + row_b, low + 64, p.K)};
+                ra[u] = {load_chunk(a + row_a, low, p.K), load_chunk(a + row_a, low + 64, p.K)};
             }
-#pragma unroll
-            for (int i = 0; i < S::kMT; ++i) sa[u][i] = p.sa[(int64_t)kb * p.M + m[i]];
-#pragma unroll
-            for (int j = 0; j < S::kNT; ++j)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int n = min(n0 + j * 16 + 4 * quarter + e, p.N - 1);
-                    sb[u][j][e] = kTiles ? p.sb[(int64_t)kb * cols_sb + n0 / kGroup] : p.sb[(int64_t)kb * cols_sb + n];
-                }
-        }
-#pragma unroll
-        for (int u = 0; u < kCount; ++u)
-#pragma unroll
-            for (int j = 0; j < S::kNT; ++j) {
-                Frag<kFmtB, kPrecise> first;
-                first.set({fb[u][j][0], fb[u][j][1]});
-#pragma unroll
-                for (int i = 0; i < S::kMT; ++i) {
-                    Frag<kFmtA, kPrecise> second;
-                    second.set({fa[u][i][0], fa[u][i][1]});
-                    const f32x4 d = block_product(first, second);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) acc[i][j][e] = fmaf(d[e], sa[u][i] * sb[u][j][e], acc[i][j][e]);
-                }
-            }
-    };
-    static_assert(kGroup % S::kN == 0, "one tile of b's scales per workgroup");
-    const int whole = p.K / kGroup;
-    int kb = wave;
-    for (; kb + (S::kAhead - 1) * S::kWaves < whole; kb += S::kAhead * S::kWaves)
-        run(kb, std::integral_constant<int, S::kAhead>{}, std::true_type{});
-    // what is left in a second and a third batch at most
-    for (; kb + S::kWaves < whole; kb += 2 * S::kWaves) run(kb, std::integral_constant<int, 2>{}, std::true_type{});
-    for (; kb < whole; kb += S::kWaves) run(kb, std::integral_constant<int, 1>{}, std::true_type{});
-    for (; kb < blocks; kb += S::kWaves) run(kb, std::integral_constant<int, 1>{}, std::false_type{});
-
-#pragma unroll
-    for (int i = 0; i < S::kMT; ++i)
-#pragma unroll
-        for (int j = 0; j < S::kNT; ++j) part[wave][i * S::kNT + j][lane] = acc[i][j];
-    __syncthreads();
-    for (int t = wave; t < S::kMT * S::kNT; t += S::kWaves) {
-        f32x4 sum = part[0][t][lane];
-#pragma unroll
-        for (int w = 1; w < S::kWaves; ++w) sum += part[w][t][lane];
-        const int row = t / S::kNT * 16 + row16, n = n0 + t % S::kNT * 16 + 4 * quarter;
-        if (row < p.M)
+            sa[u] = p.sa[(int64_t)kb * p.M + m];
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                if (n + e < p.N) {
-                    const int64_t at = (int64_t)row * p.N + n + e;
-                    if (kPrecise) {
-                        float *o = static_cast<float *>(p.out) + at;
-                        *o = p.accumulate ? *o + sum[e] : sum[e];
-                    } else {
-                        static_cast<bf16 *>(p.out)[at] = from_float<bf16>(sum[e]);
-                    }
-                }
+                sb[u][e] = p.sb[(int64_t)kb * cols + (kTiles ? n0 / kGroup : min(n0 + 4 * quarter + e, p.N - 1))];
+        }
+#pragma unroll
+        for (int u = 0; u < kCount; ++u) {
+            Frag<kFmtB, kPrecise> first;
+            Frag<kFmtA, kPrecise> second;
+            first.set(rb[u]);
+            second.set(ra[u]);
+            const f32x4 d = block_product(first, second);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[e] = fmaf(d[e], sa[u] * sb[u][e], acc[e]);
+        }
+    };
+    int kb = wave;
+    for (; kb + (kAhead - 1) * kStripWaves < whole; kb += kAhead * kStripWaves)
+        run(kb, std::integral_constant<int, kAhead>{}, std::true_type{});
+    // what is left in a second and a third batch at most
+    for (; kb + kStripWaves < whole; kb += 2 * kStripWaves) run(kb, std::integral_constant<int, 2>{}, std::true_type{});
+    for (; kb < whole; kb += kStripWaves) run(kb, std::integral_constant<int, 1>{}, std::true_type{});
+    for (; kb < blocks; kb += kStripWaves) run(kb, std::integral_constant<int, 1>{}, std::false_type{});
+
+    part[wave][lane] = acc;
+    __syncthreads();
+    if (wave > 0 || row16 >= p.M) return;
+#pragma unroll 5
+    for (int w = 1; w < kStripWaves; ++w) acc += part[w][lane];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const int n = n0 + 4 * quarter + e;
+        if (n >= p.N) break;
+        const int64_t at = (int64_t)row16 * p.N + n;
+        if constexpr (kPrecise) {
+            float *to = static_cast<float *>(p.out) + at;
+            *to = p.accumulate ? *to + acc[e] : acc[e];
+        } else {
+            static_cast<bf16 *>(p.out)[at] = from_float<bf16>(acc[e]);
+        }
     }
 }
 
@@ -663,17 +633,17 @@ using LargePrecise = Shape<2, 4, 4, 4>;  // 128 x 256
 using Medium = Shape<2, 2, 4, 4>;        // 128 x 128, two workgroups a CU
 using Low64 = Shape<2, 2, 2, 4>;         // 64 x 128
 using Low32 = Shape<1, 4, 2, 2>;         // 32 x 128
-using Strip16 = Strip<1, 1, 16, 4>;
+struct Strip {
+    static constexpr int kThreads = kStripThreads;
+};
 
 template <typename S, int kFmtA, int kFmtB, bool kTiles, bool kPrecise>
 struct Kernel {
     static const void *get() { return (const void *)&gemm_kernel<S, kFmtA, kFmtB, kTiles, kPrecise>; }
 };
-template <int kMT, int kNT, int kWaves, int kAhead, int kFmtA, int kFmtB, bool kTiles, bool kPrecise>
-struct Kernel<Strip<kMT, kNT, kWaves, kAhead>, kFmtA, kFmtB, kTiles, kPrecise> {
-    static const void *get() {
-        return (const void *)&strip_kernel<Strip<kMT, kNT, kWaves, kAhead>, kFmtA, kFmtB, kTiles, kPrecise>;
-    }
+template <int kFmtA, int kFmtB, bool kTiles, bool kPrecise>
+struct Kernel<Strip, kFmtA, kFmtB, kTiles, kPrecise> {
+    static const void *get() { return (const void *)&strip_kernel<kFmtA, kFmtB, kTiles, kPrecise>; }
 };
 template <typename S, bool kPrecise, int kFmtA, int kFmtB>
 const void *pick(bool tiles) {
@@ -707,8 +677,8 @@ struct Plan {
 // in one; 4096 x 4096, K = 4096: 109 us in 2 runs, 69 us in one).
 constexpr int kCus = 256;
 Plan plan_of(int64_t M, int64_t N, int64_t K, bool precise) {
-    Plan plan = {Way::kStrip, 16, 16, 1, 0, 0};
-    if (M <= 16) return plan;
+    Plan plan = {Way::kStrip, kStrip, kStrip, 1, 0, 0};
+    if (M <= kStrip) return plan;
     struct Kind {
         Way way;
         int m, n, per_cu;
@@ -754,15 +724,21 @@ bool bad_gemm(int64_t M, int64_t N, int64_t K) {
            ceil_div(M, 32) * ceil_div(N, 128) > (int64_t)0x7FFFFFFF / 16;
 }
 
+// What a product's sizes, output type and flags are refused for.
+int check_gemm(int64_t M, int64_t N, int64_t K, int out_dtype, uint32_t flags) {
+    if (bad_gemm(M, N, K)) return FP4Q_ERR_SHAPE;
+    if (flags & ~(uint32_t)(FP4Q_FLAG_TILES | FP4Q_FLAG_ACCUMULATE)) return FP4Q_ERR_ARG;
+    if (out_dtype == FP4Q_OUT_F32) return FP4Q_OK;
+    return out_dtype == FP4Q_OUT_BF16 && !(flags & FP4Q_FLAG_ACCUMULATE) ? FP4Q_OK : FP4Q_ERR_ARG;
+}
+
 }  // namespace
 
 extern "C" {
 
 int fp4q_gemm8_workspace(int64_t M, int64_t N, int64_t K, int out_dtype, uint32_t flags, size_t *bytes) {
-    if (bad_gemm(M, N, K)) return FP4Q_ERR_SHAPE;
-    if (flags & ~(uint32_t)(FP4Q_FLAG_TILES | FP4Q_FLAG_ACCUMULATE)) return FP4Q_ERR_ARG;
-    if (out_dtype != FP4Q_OUT_F32 && (out_dtype != FP4Q_OUT_BF16 || (flags & FP4Q_FLAG_ACCUMULATE)))
-        return FP4Q_ERR_ARG;
+    const int st = check_gemm(M, N, K, out_dtype, flags);
+    if (st != FP4Q_OK) return st;
     if (!bytes) return FP4Q_ERR_NULL;
     *bytes = M && N ? plan_of(M, N, K, out_dtype == FP4Q_OUT_F32).workspace : 0;
     return FP4Q_OK;
@@ -772,15 +748,18 @@ int fp4q_gemm8(const uint8_t *a, int64_t a_pitch, int a_format, const float *a_s
                const uint8_t *b, int64_t b_pitch, int b_format, const float *b_scales, int64_t M,
                int64_t N, int64_t K, void *out, int out_dtype, uint32_t flags, void *workspace,
                size_t workspace_bytes, void *stream) {
-    size_t need = 0;
-    if (bad_gemm(M, N, K)) return FP4Q_ERR_SHAPE;
-    if (K > 0 && (a_pitch < K || b_pitch < K || a_pitch >= (1 << 23) || b_pitch >= (1 << 23))) return FP4Q_ERR_SHAPE;
-    const int st = fp4q_gemm8_workspace(M, N, K, out_dtype, flags, &need);
+    if (!bad_gemm(M, N, K) && K > 0 &&
+        (a_pitch < K || b_pitch < K || a_pitch >= (1 << 23) || b_pitch >= (1 << 23)))
+        return FP4Q_ERR_SHAPE;
+    const int st = check_gemm(M, N, K, out_dtype, flags);
     if (st != FP4Q_OK) return st;
     const bool add = flags & FP4Q_FLAG_ACCUMULATE, tiles = flags & FP4Q_FLAG_TILES;
     if ((a_format != FP4Q_E4M3 && a_format != FP4Q_E5M2) || (b_format != FP4Q_E4M3 && b_format != FP4Q_E5M2))
         return FP4Q_ERR_ARG;
     if (M == 0 || N == 0) return FP4Q_OK;
+    const bool precise = out_dtype == FP4Q_OUT_F32;
+    const Plan plan = plan_of(M, N, K, precise);
+    const size_t need = plan.workspace;
     if (!out || (K > 0 && (!a || !a_scales || !b || !b_scales)) || (need && !workspace)) return FP4Q_ERR_NULL;
     if (!aligned(out, 16) || !aligned(workspace, 16)) return FP4Q_ERR_ALIGN;
     if (K > 0 && (!aligned(a, 16) || !aligned(b, 16) || a_pitch % 16 || b_pitch % 16)) return FP4Q_ERR_ALIGN;
@@ -792,10 +771,8 @@ int fp4q_gemm8(const uint8_t *a, int64_t a_pitch, int a_format, const float *a_s
                          rng(a_scales, 4 * groups * M),
                          rng(b_scales, 4 * groups * (tiles ? ceil_div(N, kGroup) : N))};
     if (clash(outs, 2, ins, K > 0 ? 4 : 0)) return FP4Q_ERR_ARG;
-    const bool precise = out_dtype == FP4Q_OUT_F32;
-    const Plan plan = plan_of(M, N, K, precise);
     GemmArgs p = {a, b, a_scales, b_scales, out, a_pitch, b_pitch, (int)M, (int)N, (int)K,
-                  (int)ceil_div(M, plan.tile_m), (int)ceil_div(N, plan.tile_n), precise, add,
+                  (int)ceil_div(M, plan.tile_m), (int)ceil_div(N, plan.tile_n), add,
                   plan.parts, plan.part_size, static_cast<float *>(workspace)};
     void *args[] = {&p};
     const void *fn = nullptr;
@@ -808,7 +785,7 @@ int fp4q_gemm8(const uint8_t *a, int64_t a_pitch, int a_format, const float *a_s
         threads = Fast::kThreads;
     };
     switch (plan.way) {
-        case Way::kStrip: use(Strip16{}, Strip16{}); break;
+        case Way::kStrip: use(Strip{}, Strip{}); break;
         case Way::kLow32: use(Low32{}, Low32{}); break;
         case Way::kLow64: use(Low64{}, Low64{}); break;
         case Way::kMedium: use(Medium{}, Medium{}); break;
