@@ -52,20 +52,20 @@ def _lib() -> ctypes.CDLL:
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _launch_stream(stream, device):
-    """The address of the HIP stream to launch on (see _stream)."""
+def _launch_stream(stream, index):
+    """The address of the HIP stream to launch on (see _stream), on the GPU of that index."""
     if stream is None and _raw_stream is not None:
-        return _raw_stream(device.index)
-    return _stream(stream, device)
+        return _raw_stream(index)
+    return _stream(stream, torch.device("cuda", index))
 
 
 def _gpu(*tensors):
-    """The one GPU that every tensor argument (None apart) lies on."""
+    """The index of the one GPU that every tensor argument (None apart) lies on."""
     first = tensors[0].get_device()
     for t in tensors:
-        if t is not None and (t.get_device() != first or first < 0):
+        if t is not None and t.get_device() != first or first < 0:
             raise ValueError("fp4q: every tensor must be on the same GPU (%s, %s)" % (tensors[0].device, t.device))
-    return tensors[0].device
+    return first
 
 
 @functools.lru_cache(maxsize=4096)
@@ -82,15 +82,18 @@ def _groups(n: int) -> int:
 
 def _like(t, name, shape, dtype):
     """A tensor argument of exactly this shape and type, contiguous."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.is_contiguous():
+            return t
+    except AttributeError:
+        pass
     if not isinstance(t, torch.Tensor):
         raise TypeError("fp4q: %s must be a torch tensor" % name)
     if t.dtype is not dtype:
         raise TypeError("fp4q: %s must be %s, got %s" % (name, dtype, t.dtype))
     if t.shape != shape:
         raise ValueError("fp4q: %s must have shape %s, has %s" % (name, tuple(shape), tuple(t.shape)))
-    if not t.is_contiguous():
-        raise ValueError("fp4q: %s must be contiguous" % name)
-    return t
+    raise ValueError("fp4q: %s must be contiguous" % name)
 
 
 def _typed(t, name):
@@ -137,6 +140,8 @@ def _codes_in(t, name):
     if t.dim() != 2:
         raise ValueError("fp4q: expected a 2-D tensor [rows, cols]")
     rows, cols = t.shape
+    if cols % 16 == 0 and t.is_contiguous():
+        return fmt, rows, cols, cols
     wide = (cols + 15) // 16 * 16
     pitch = t.stride(0) if rows > 1 else wide
     if rows and cols:
