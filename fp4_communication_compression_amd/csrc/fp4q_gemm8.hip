@@ -673,13 +673,15 @@ struct Plan {
 
 // The tile and the number of runs that K is cut into: the least of an estimate made of
 // what the kernels take on this card.  A tile's block costs block_us with one, two or
-// three workgroups on a CU (measured at K = 4096 and 8192 with 256, 512 and 768 tiles; a
-// workgroup's beginning and end cost start_us besides), so large tiles serve large
-// outputs (8192 x 11008, K = 4096: 366 us in 256 x 256 tiles, 421 us in 128 x 128) and
-// small ones fill the card when the output is small (1000 x 4096, K = 4096: 27 us in
-// 64 x 128 tiles, 39 us in 256 x 256).  Cutting K fills it further, for a second launch
-// and one write and read of every run's sums (32 x 4096, K = 4096: 11 us in 4 runs, 19 us
-// in one; 4096 x 4096, K = 4096: 109 us in 2 runs, 69 us in one).
+// three workgroups on a CU and its beginning and end cost start_us besides: fitted to the
+// times of every tile with 1 to 16 runs over 44 products (17 x 4096 to 8192 x 4096, K from
+// 1000 to 16384, both output types; over these the choice takes 1.6 % longer than the best
+// way on average, 20 % at most).  So large tiles serve large outputs (8192 x 11008,
+// K = 4096: 376 us in 256 x 256 tiles, 419 us in 128 x 128) and small ones fill the card
+// when the output is small (1000 x 4096, K = 4096: 25.5 us in 64 x 128 tiles, 39 us in
+// 256 x 256).  Cutting K fills it further, for a second launch and one write and read of
+// every run's sums (17 x 4096, K = 4096: 10.2 us in 6 runs, 12.7 in 16, 19 in one;
+// 2047 x 4096, K = 11008: 101 us in 256 x 256 tiles with 2 runs, 92 us in 128 x 128 with one).
 constexpr int kCus = 256;
 Plan plan_of(int64_t M, int64_t N, int64_t K, bool precise) {
     Plan plan = {Way::kStrip, kStrip, kStrip, 1, 0, 0};
@@ -689,15 +691,15 @@ Plan plan_of(int64_t M, int64_t N, int64_t K, bool precise) {
         int m, n, per_cu;
         double start_us, block_us[3];
     };
-    static const Kind fast[] = {{Way::kLow32, 32, 128, 3, 2.5, {0.48, 0.53, 0.69}},
-                                {Way::kLow64, 64, 128, 3, 2.5, {0.54, 0.74, 1.0}},
-                                {Way::kMedium, 128, 128, 2, 4.0, {0.72, 1.13}},
-                                {Way::kLarge, 256, 256, 1, 5.5, {1.75}}};
-    static const Kind exact[] = {{Way::kLow32, 32, 128, 3, 2.5, {0.66, 0.82, 1.1}},
-                                 {Way::kLow64, 64, 128, 2, 2.5, {0.94, 1.23}},
-                                 {Way::kMedium, 128, 128, 2, 4.0, {1.4, 1.98}},
-                                 {Way::kLarge, 128, 256, 1, 5.5, {2.0}}};
-    constexpr double kLaunchUs = 2.5, kJoinUsPerSum = 0.95e-6;
+    static const Kind fast[] = {{Way::kLow32, 32, 128, 3, 0.6, {0.45, 0.53, 0.69}},
+                                {Way::kLow64, 64, 128, 3, 1.5, {0.48, 0.62, 0.93}},
+                                {Way::kMedium, 128, 128, 2, 2.6, {0.62, 0.98}},
+                                {Way::kLarge, 256, 256, 1, 5.7, {1.54}}};
+    static const Kind exact[] = {{Way::kLow32, 32, 128, 3, 0.6, {0.52, 0.73, 0.94}},
+                                 {Way::kLow64, 64, 128, 2, 0.5, {0.75, 1.05}},
+                                 {Way::kMedium, 128, 128, 2, 1.9, {1.16, 1.75}},
+                                 {Way::kLarge, 128, 256, 1, 4.4, {1.68}}};
+    constexpr double kLaunchUs = 4.7, kJoinUs = 1.5, kJoinUsPerPart = 0.25, kJoinUsPerSum = 1.1e-6;
     const int64_t blocks = ceil_div(K, kGroup);
     double best = 1e300;
     for (const Kind &k : precise ? exact : fast) {
@@ -707,7 +709,7 @@ Plan plan_of(int64_t M, int64_t N, int64_t K, bool precise) {
             const double run = (double)ceil_div(blocks, parts);
             double us = kLaunchUs + full * (k.start_us + run * k.block_us[k.per_cu - 1]);
             if (rest) us += k.start_us + run * k.block_us[ceil_div(rest, kCus) - 1];
-            if (parts > 1) us += kLaunchUs + kJoinUsPerSum * M * N * parts;
+            if (parts > 1) us += kJoinUs + (kJoinUsPerPart + kJoinUsPerSum * M * N) * parts;
             if (us < best) {
                 best = us;
                 plan.way = k.way;
