@@ -6,8 +6,15 @@
 //
 // b is the matrix core's first operand: a lane then holds four neighbouring n of
 // one m, a's scale is one value per lane, and the output leaves in pieces of four
-// neighbours.  A block's sum over its 128 k is scaled by the block's two scales
-// and added to the fp32 accumulators.
+// neighbours.  A block's sum over its 128 k is multiplied by b's scale, then by a's,
+// and added to the fp32 accumulators.  The product of the two scales is never taken
+// by itself: it can leave fp32's range where the scaled sum does not (a sum of 0
+// under two scales of 2^70 is 0, not 0 infinity).  A scale of a row of b is a
+// multiplication after the matrix core.  The scale of a tile of b, one for all of a
+// wavefront's columns, is split: its power of two goes into the matrix core's
+// products, its rest to a's scales, with no work on the sums.  8192 x 11008,
+// K = 4096 takes 361 us so, 408 with a multiplication of the sums (on a card where
+// the product of the scales took 352); 2047 x 4096, K = 11008 92, 106 and 89.
 //
 // Two ways to the block's sum:
 //   8-bit matrix core  (bf16 output) one v_mfma_f32_16x16x128_f8f6f4 covers the
@@ -62,13 +69,26 @@ struct GemmArgs {
 struct Raw {
     u32x4 low, high;
 };
-// ... and as the matrix core takes them.
+// A scale as a power of two times the rest, 1 <= |rest| < 2: a finite value of an operand
+// over its scale's rest is finite.  Scales below 2^-100 leave more to the rest (a code times
+// the power is a normal bf16), and zero, infinity and NaN are all rest.
+struct Split {
+    int powers;  // byte 0: the power's exponent, biased as in fp32; byte 2: that of 1
+    float rest;
+    __device__ __forceinline__ void set(float scale) {
+        const int e = max(__builtin_amdgcn_frexp_expf(scale), -99);  // scale = rest 2^(e - 1)
+        powers = e + (126 | 127 << 16);
+        rest = ldexpf(scale, 1 - e);
+    }
+    __device__ __forceinline__ float factor() const { return __uint_as_float((unsigned)powers << 23); }
+};
+// ... and as the matrix core takes them, times a power of two.
 template <int kFmt, bool kPrecise>
 struct Frag;
 template <int kFmt>
 struct Frag<kFmt, false> {
     i32x8 v;
-    __device__ __forceinline__ void set(const Raw &raw) {
+    __device__ __forceinline__ void set(const Raw &raw, float = 1.0f) {  // (block_product takes the power here)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             v[i] = (int)raw.low[i];
@@ -79,17 +99,17 @@ struct Frag<kFmt, false> {
 template <int kFmt>
 struct Frag<kFmt, true> {
     bf16x8 v[4];
-    __device__ __forceinline__ void set(const Raw &raw) {
+    __device__ __forceinline__ void set(const Raw &raw, float power = 1.0f) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const unsigned w = i < 4 ? raw.low[i] : raw.high[i - 4];
             bf16x2 p, q;
             if constexpr (kFmt == FP4Q_E4M3) {
-                p = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, false);
-                q = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, true);
+                p = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, power, false);
+                q = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, power, true);
             } else {
-                p = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(w, 1.0f, false);
-                q = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(w, 1.0f, true);
+                p = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(w, power, false);
+                q = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(w, power, true);
             }
             const int at = 4 * (i & 1);
             v[i >> 1][at] = p[0];
@@ -100,15 +120,20 @@ struct Frag<kFmt, true> {
     }
 };
 
-// One block's product of a 16 x 16 tile.
-template <int kFirst, int kSecond>
-__device__ __forceinline__ f32x4 block_product(const Frag<kFirst, false> &first, const Frag<kSecond, false> &second) {
+// One block's product of a 16 x 16 tile.  With kScaled the 8-bit matrix core's products take
+// the powers of two in bytes 0 (for `first`) and 2 (for `second`) of powers.
+template <bool kScaled, int kFirst, int kSecond>
+__device__ __forceinline__ f32x4 block_product(const Frag<kFirst, false> &first, const Frag<kSecond, false> &second,
+                                               int powers) {
+    constexpr f32x4 kZero = {0, 0, 0, 0};
+    if constexpr (kScaled)
+        return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(first.v, second.v, kZero, kFirst, kSecond, 0, powers,
+                                                                2, powers);
     // with scale operands 0 this is the instruction without the matrix core's own scaling
-    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(first.v, second.v, f32x4{0, 0, 0, 0}, kFirst, kSecond,
-                                                            0, 0, 0, 0);
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(first.v, second.v, kZero, kFirst, kSecond, 0, 0, 0, 0);
 }
-template <int kFirst, int kSecond>
-__device__ __forceinline__ f32x4 block_product(const Frag<kFirst, true> &first, const Frag<kSecond, true> &second) {
+template <bool kScaled, int kFirst, int kSecond>
+__device__ __forceinline__ f32x4 block_product(const Frag<kFirst, true> &first, const Frag<kSecond, true> &second, int) {
     f32x4 d = {0, 0, 0, 0};
 #pragma unroll
     for (int i = 0; i < 4; ++i) d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(first.v[i], second.v[i], d, 0, 0, 0);
@@ -286,6 +311,7 @@ struct Tile {
     struct Head {
         Raw b[S::kTilesN], a;
         float sa, sb;
+        Split tile;  // sb, with kTiles
     };
     __device__ __forceinline__ void read_head(const Stage<S> &in, Head &h, int item) {
         if (item == 0) {
@@ -327,6 +353,8 @@ struct Tile {
         Frag<kFmtB, kPrecise> fb[kTilesN];
         float sa[kTilesM];
         f32x4 sb[kTilesN], d[kLag + 1];
+        const float factor = kTiles ? h.tile.factor() : 1.0f;
+        const int powers = kTiles ? h.tile.powers : 0;
         ra[0] = h.a;
         sa[0] = h.sa;
 #pragma unroll
@@ -363,18 +391,19 @@ struct Tile {
                 // fragments are made where their first product needs them, and the next row's
                 // while the matrix core works on this one's
                 if constexpr (t == 0) fa[0].set(ra[0]);
-                if constexpr (i == 0) fb[j].set(h.b[j]);
-                d[t % (kLag + 1)] = block_product(fb[j], fa[i & 1]);
+                if constexpr (i == 0) fb[j].set(h.b[j], factor);
+                d[t % (kLag + 1)] = block_product<kTiles>(fb[j], fa[i & 1], powers);
             }
             __builtin_amdgcn_sched_barrier(0);  // the matrix core first
+            if constexpr (kTiles && t == kCount - 1) n.tile.set(n.sb);
             if constexpr (j == kTilesN - 1 && i + 1 < kTilesM) fa[(i + 1) & 1].set(ra[i + 1]);
             if constexpr (t >= kLag) {
                 constexpr int ui = (t - kLag) / kTilesN, uj = (t - kLag) % kTilesN;
-                if constexpr (kTiles && uj == 0) sa[ui] *= h.sb;
+                if constexpr (kTiles && uj == 0) sa[ui] *= h.tile.rest;
                 const f32x4 v = d[(t - kLag) % (kLag + 1)];
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    acc[ui][uj][e] = fmaf(v[e], kTiles ? sa[ui] : sa[ui] * sb[uj][e], acc[ui][uj][e]);
+                    acc[ui][uj][e] = fmaf(kTiles ? v[e] : v[e] * sb[uj][e], sa[ui], acc[ui][uj][e]);
             }
             __builtin_amdgcn_sched_barrier(0);
         });
@@ -488,6 +517,7 @@ __global__ __launch_bounds__(S::kThreads, 2) void gemm_kernel(GemmArgs p) {
             }
         }
         static_for<t.kHeadB + 1>([&](auto i) FP4Q_INLINE { t.read_head(even, h0, i.value); });
+        if constexpr (kTiles) h0.tile.set(h0.sb);
         for (; kb + 1 < end; kb += 2) {
             t.step(even, odd, h0, h1, kb, end, ragged);
             t.step(odd, even, h1, h0, kb + 1, end, ragged);
@@ -601,9 +631,9 @@ __global__ __launch_bounds__(kStripThreads, kTiles && !kPrecise ? 8 : 4) void st
             Frag<kFmtA, kPrecise> second;
             first.set(rb[u]);
             second.set(ra[u]);
-            const f32x4 d = block_product(first, second);
+            const f32x4 d = block_product<false>(first, second, 0);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) acc[e] = fmaf(d[e], sa[u] * sb[u][e], acc[e]);
+            for (int e = 0; e < 4; ++e) acc[e] = fmaf(d[e] * sb[u][e], sa[u], acc[e]);
         }
     };
     int kb = wave;

@@ -103,11 +103,13 @@ int fp4q_quantize8(const void *x, int64_t rows, int64_t cols, int dtype, int for
 
 /* out[m][n] = sum over k of a[m][k] b[n][k], of the operands' values: a [M x K]
  * with rows of 128, b [N x K] with rows of 128 or (FP4Q_FLAG_TILES) tiles.
- * The sum over a block of 128 comes from the matrix cores, block sums are scaled
- * and added in fp32.  With fp32 output the matrix core works on the codes' values
- * in bf16 (exact products, fp32 sums); with bf16 output on the codes themselves,
- * twice as fast, where it drops what lies below 2^-13 of the largest of 8
- * neighbouring products (about 2e-5 of the result, a hundredth of bf16's rounding).
+ * The sum over a block of 128 comes from the matrix cores; it is multiplied by b's
+ * scale, then by a's, and added in fp32.  In every block the products of a's codes
+ * with b's values must sum to a finite fp32 value; the product of the two scales
+ * need not be one.  With fp32 output the matrix core works on the codes' values in
+ * bf16 (exact products, fp32 sums); with bf16 output on the codes themselves, twice
+ * as fast, where it drops what lies below 2^-13 of the largest of 8 neighbouring
+ * products (about 2e-5 of the result, a hundredth of bf16's rounding).
  *   forward        a = activations, b = weight [out x in]
  *   input gradient a = output gradient, b = the transposed weight (codes_t)
  *   weight gradient a = the transposed output gradient, b = the transposed

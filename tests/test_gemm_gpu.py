@@ -1,0 +1,69 @@
+"""The 8-bit product on the GPU where its arithmetic and its kernels can go wrong: scales far
+from 1."""
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from tests import linear_ref as ref
+from tests.test_linear_gpu import check_bf16, fp4q, up, within  # noqa: F401 (fp4q is the fixture)
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+E4M3, E5M2 = torch.float8_e4m3fn, torch.float8_e5m2
+BF16, F32 = torch.bfloat16, torch.float32
+
+# every kernel of the product: few rows, and each size of tile
+SIZES = [(5, 300), (40, 300), (1030, 4100), (2047, 4096), (4000, 4096)]
+
+
+def scales(gen, k, rows, power):
+    return (torch.rand(ref.groups(k), rows, generator=gen) + 1) * 2.0 ** power
+
+
+@pytest.mark.parametrize("m,n", SIZES)
+@pytest.mark.parametrize("tiles", [True, False])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_scales_whose_product_overflows(fp4q, m, n, tiles, dtype):
+    """Scales of 2^70 on both sides of a block whose sum is 0, and of 2^70 against 2^-70:
+    every sum is finite.  (A block of zeros between large values has such a scale.)"""
+    print(m, n, tiles, dtype, flush=True)
+    gen, k = torch.Generator().manual_seed(m), 300
+    a, b = ref.fake_codes(gen, m, k, E4M3), ref.fake_codes(gen, n, k, E4M3)
+    a.view(torch.uint8)[::2, :128] = 0
+    sa, sb = scales(gen, k, m, 0), scales(gen, k, ref.groups(n) if tiles else n, 0)
+    sa[0, ::2] *= 2.0 ** 70
+    sa[0, 1::2] *= 2.0 ** -70
+    sb[0] *= 2.0 ** 70
+    sa[2] *= 2.0 ** 90
+    sb[2] *= 2.0 ** -90
+    got = fp4q.fp4q_gemm8(up(a), sa.to(DEV), up(b), sb.to(DEV), out_dtype=dtype).cpu()
+    rows = torch.unique(torch.cat([torch.arange(0, m, 61), torch.arange(max(0, m - 9), m)]))
+    part = a[rows], sa[:, rows], b, sb
+    if dtype == F32:
+        within(got[rows], *ref.gemm(*part))
+    else:
+        check_bf16(got[rows], *part)
+    assert bool(got.isfinite().all())
+
+
+@pytest.mark.parametrize("m,n", SIZES)
+@pytest.mark.parametrize("tiles", [True, False])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_scales_whose_product_underflows(fp4q, m, n, tiles, dtype):
+    """Scales of 2^-73 on both sides under sums of 2^24: the results are normal numbers, the
+    scales' product is not."""
+    print(m, n, tiles, dtype, flush=True)
+    gen, k = torch.Generator().manual_seed(m + 1), 300
+    a, b = ref.fake_codes(gen, m, k, E5M2), ref.fake_codes(gen, n, k, E4M3)
+    a.copy_((torch.randn(m, k, generator=gen) * 10000).to(E5M2))
+    b.copy_((torch.randn(n, k, generator=gen) * 80).clamp(-448, 448).to(E4M3))
+    sa, sb = scales(gen, k, m, -73), scales(gen, k, ref.groups(n) if tiles else n, -73)
+    got = fp4q.fp4q_gemm8(up(a), sa.to(DEV), up(b), sb.to(DEV), out_dtype=dtype).cpu()
+    rows = torch.unique(torch.cat([torch.arange(0, m, 61), torch.arange(max(0, m - 9), m)]))
+    part = a[rows], sa[:, rows], b, sb
+    want, off = ref.gemm(*part)
+    if dtype == F32:
+        # and where a step or the result lies below the normal numbers, half of 2^-149 each
+        within(got[rows], want, off + 8 * 2.0 ** -150)
+    else:
+        within(got[rows], want, ref.gemm_bf16_off(*part, want) + 8 * 2.0 ** -150 + 2.0 ** -134)
