@@ -20,8 +20,11 @@
 //   8-bit matrix core  (bf16 output) one v_mfma_f32_16x16x128_f8f6f4 covers the
 //     block of a 16 x 16 tile.  It adds the products of 8 neighbouring k at the
 //     largest one's exponent and drops what lies below 2^-13 of it (seen with
-//     powers of two; groups of 8 are added in fp32): about 2e-5 of the result,
-//     a hundredth of the output's own rounding.
+//     powers of two; groups of 8 are added in fp32): at most 7 2^-13 of each
+//     group's largest product (2.1 2^-13 seen on groups of two large products that
+//     cancel and six small ones, there two thirds of the result).  Over normal
+//     values it is about 2e-5 of the result, a hundredth of the output's own
+//     rounding: that is why bf16 output takes it, and fp32 output does not.
 //   16-bit matrix core (fp32 output) the codes become bf16, which holds every
 //     E4M3 and E5M2 value, and four v_mfma_f32_16x16x32_bf16 add their exact
 //     products in fp32: half the rate, 1e-8 per block.

@@ -268,7 +268,9 @@ def fp4q_gemm8(a, a_scales, b, b_scales, out=None, out_dtype=None, accumulate: b
     """The product of two 8-bit operands: a [M, K] with a_scales [ceil(K / 128), M] and
     b [N, K] with b_scales [ceil(K / 128), N] or, for tiles, [ceil(K / 128), ceil(N / 128)]
     -> [M, N] float32 or bfloat16 (bfloat16 when neither ``out`` nor ``out_dtype`` says
-    otherwise).  ``accumulate`` adds the product to a float32 ``out``."""
+    otherwise).  ``accumulate`` adds the product to a float32 ``out``.  A bfloat16 product
+    drops, of every 8 neighbouring products, what lies below 2^-13 of the largest: sums in
+    which large products cancel want float32 output."""
     fa, M, K, a_pitch = _codes_in(a, "a")
     fb, N, kb, b_pitch = _codes_in(b, "b")
     if kb != K:

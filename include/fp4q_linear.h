@@ -107,9 +107,12 @@ int fp4q_quantize8(const void *x, int64_t rows, int64_t cols, int dtype, int for
  * scale, then by a's, and added in fp32.  In every block the products of a's codes
  * with b's values must sum to a finite fp32 value; the product of the two scales
  * need not be one.  With fp32 output the matrix core works on the codes' values in
- * bf16 (exact products, fp32 sums); with bf16 output on the codes themselves, twice
- * as fast, where it drops what lies below 2^-13 of the largest of 8 neighbouring
- * products (about 2e-5 of the result, a hundredth of bf16's rounding).
+ * bf16 (exact products, fp32 sums).  With bf16 output it works on the codes
+ * themselves, twice as fast, and drops what lies below 2^-13 of the largest of 8
+ * neighbouring products (k = 8 i .. 8 i + 7): of each 8 at most 7 * 2^-13 of the
+ * largest one.  Over normally distributed values that is about 2e-5 of the result, a
+ * hundredth of bf16's rounding; where large products cancel, it can be most of the
+ * result.  Such sums (outliers of both signs) want fp32 output.
  *   forward        a = activations, b = weight [out x in]
  *   input gradient a = output gradient, b = the transposed weight (codes_t)
  *   weight gradient a = the transposed output gradient, b = the transposed

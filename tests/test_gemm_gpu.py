@@ -1,5 +1,5 @@
 """The 8-bit product on the GPU where its arithmetic and its kernels can go wrong: scales far
-from 1."""
+from 1, products that cancel."""
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -67,3 +67,51 @@ def test_scales_whose_product_underflows(fp4q, m, n, tiles, dtype):
         within(got[rows], want, off + 8 * 2.0 ** -150)
     else:
         within(got[rows], want, ref.gemm_bf16_off(*part, want) + 8 * 2.0 ** -150 + 2.0 ** -134)
+
+
+@pytest.mark.parametrize("m,n", [(5, 300), (40, 300), (2047, 4096), (4000, 4096)])
+@pytest.mark.parametrize("fa", [E4M3, E5M2])
+@pytest.mark.parametrize("tiles", [True, False])
+def test_cancelling_products(fp4q, m, n, fa, tiles):
+    """Of 8 neighbouring products two large ones cancel and the result is the sum of the small
+    ones: bf16 output is off by at most 7 * 2^-13 of each group's largest product (and its own
+    rounding), fp32 output by fp32's rounding alone."""
+    print(m, n, fa, tiles, flush=True)
+    k, gen = 256, torch.Generator().manual_seed(m)
+    a, b = ref.fake_codes(gen, m, k, fa), ref.fake_codes(gen, n, k, E4M3)
+    va, vb = torch.zeros(m, k), torch.zeros(n, k)
+    for g in range(0, k, 8):
+        at = (torch.randperm(8, generator=gen) + g).tolist()
+        large = 2.0 ** torch.randint(4, 9, (m,), generator=gen)
+        va[:, at[0]], va[:, at[1]] = large, -large
+        vb[:, at[0]] = vb[:, at[1]] = 256
+        for i in at[2:]:
+            va[:, i] = 2.0 ** (6 * torch.rand(m, generator=gen) - 4)
+            vb[:, i] = 2.0 ** (5 * torch.rand(n, generator=gen) - 2)
+    a.copy_(va.to(fa))
+    b.copy_(vb.to(E4M3))
+    sa, sb = scales(gen, k, m, 0), scales(gen, k, ref.groups(n) if tiles else n, 0)
+    rows = torch.unique(torch.cat([torch.arange(0, m, 193), torch.arange(max(0, m - 9), m)]))
+    part = a[rows], sa[:, rows], b, sb
+    want, off = ref.gemm(*part)
+    dev = up(a), sa.to(DEV), up(b), sb.to(DEV)
+    within(fp4q.fp4q_gemm8(*dev, out_dtype=F32).cpu()[rows], want, off)
+    xa, xb = ref.values(*part[:2]), ref.values(*part[2:])
+    for g in range(0, k, 8):
+        top = torch.zeros_like(want)
+        for i in range(g, g + 8):
+            top = torch.maximum(top, (xa[:, i, None] * xb[None, :, i]).abs())
+        off = off + 7 * 2.0 ** -13 * top
+    half = ref.HALF_STEP[BF16]
+    within(fp4q.fp4q_gemm8(*dev).cpu()[rows], want, off + half * (want.abs() + off))
+
+
+def test_a_cancelled_sum_alone(fp4q):
+    """448 * 448 - 448 * 448 + 2 * 2: fp32 output is exact, bf16 output within the bound."""
+    a, b = torch.zeros(1, 128), torch.zeros(1, 128)
+    a[0, :3] = torch.tensor([448.0, -448.0, 2.0])
+    b[0, :3] = torch.tensor([448.0, 448.0, 2.0])
+    one = torch.ones(1, 1, device=DEV)
+    dev = a.to(E4M3).to(DEV), one, b.to(E4M3).to(DEV), one
+    assert float(fp4q.fp4q_gemm8(*dev, out_dtype=F32)) == 4.0
+    assert abs(float(fp4q.fp4q_gemm8(*dev)) - 4.0) <= 7 * 2.0 ** -13 * 448 * 448
