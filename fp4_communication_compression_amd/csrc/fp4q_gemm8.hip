@@ -179,14 +179,18 @@ __device__ __forceinline__ void load_to_lds(void *to, const void *from, int byte
                               (unsigned)__builtin_amdgcn_readfirstlane((int)((base >> 32) & 0xFFFF)),
                               (unsigned)__builtin_amdgcn_readfirstlane(max(bytes, 0)), 0x00020000u};
     const int at = __builtin_amdgcn_readfirstlane((int)(unsigned)(uintptr_t)(lds_void *)to);
-    // M0 holds the address in LDS; the compiler keeps nothing in it from one instruction to
-    // the next.  Then the wait states between scalar writes and the load that reads them.
+    // M0 holds the address in LDS; then the wait states between scalar writes and the load
+    // that reads them.  The compiler warns that it does not keep M0 across the assembly: it
+    // need not, only to know that M0 is written.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
     if constexpr (kBytes == 16)
         asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
-                     : : "s"(at), "v"(offset), "s"(descriptor) : "memory");
+                     : : "s"(at), "v"(offset), "s"(descriptor) : "m0", "memory");
     else
         asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dword %1, %2, 0 offen lds"
-                     : : "s"(at), "v"(offset), "s"(descriptor) : "memory");
+                     : : "s"(at), "v"(offset), "s"(descriptor) : "m0", "memory");
+#pragma clang diagnostic pop
 }
 
 // A meeting of the workgroup's wavefronts, each with at most kLeft of its loads into LDS
