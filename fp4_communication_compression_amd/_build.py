@@ -9,7 +9,7 @@ ROOT = os.path.dirname(HERE)
 SOURCES = [os.path.join(HERE, "csrc", n)
            for n in ("fp4q.hip", "fp4q_norm.hip", "fp4q_quant8.hip", "fp4q_gemm8.hip")]
 HEADERS = [os.path.join(ROOT, "include", "fp4q.h"), os.path.join(ROOT, "include", "fp4q_linear.h"),
-           os.path.join(HERE, "csrc", "fp4q_numerics.h"), os.path.join(HERE, "csrc", "fp4q_f8.h")]
+           *(os.path.join(HERE, "csrc", n) for n in ("fp4q_numerics.h", "fp4q_f8.h", "fp4q_gemm8_plan.h"))]
 LIB = os.path.join(HERE, "libfp4q.so")
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

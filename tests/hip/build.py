@@ -1,8 +1,9 @@
 """Builds the test and measurement HIP libraries in place (gfx950, the product
 library's hipcc flags): libfp4q_instr_check.so (exhaustive sweeps of the
-kernels' rounding primitives, for tests/test_gpu_instructions.py) and
+kernels' rounding primitives, for tests/test_gpu_instructions.py),
 libfp4q_twins.so (compute-free traffic twins of the kernels, for bench.py's
-ceilings leg)."""
+ceilings leg) and libfp4q_gemm8_plan.so (host code only: which kernel a product
+runs on, for tests/test_gemm_plan.py)."""
 from __future__ import annotations
 
 import os
@@ -11,7 +12,8 @@ import sys
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(os.path.dirname(HERE))
-LIBS = {"libfp4q_instr_check.so": "fp4q_instr_check.hip", "libfp4q_twins.so": "fp4q_twins.hip"}
+LIBS = {"libfp4q_instr_check.so": "fp4q_instr_check.hip", "libfp4q_twins.so": "fp4q_twins.hip",
+        "libfp4q_gemm8_plan.so": "fp4q_gemm8_plan.hip"}
 
 
 def build() -> list:

@@ -1,9 +1,10 @@
-"""The 8-bit product on the GPU where its arithmetic and its kernels can go wrong: scales far
-from 1, products that cancel."""
+"""The 8-bit product on the GPU where its arithmetic and its kernels can go wrong: every
+kernel on several blocks of K, scales far from 1, products that cancel."""
 import pytest
 
 torch = pytest.importorskip("torch")
 
+from tests import gemm_shapes
 from tests import linear_ref as ref
 from tests.test_linear_gpu import check_bf16, fp4q, up, within  # noqa: F401 (fp4q is the fixture)
 
@@ -11,6 +12,69 @@ pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
 E4M3, E5M2 = torch.float8_e4m3fn, torch.float8_e5m2
 BF16, F32 = torch.bfloat16, torch.float32
+
+def codes(gen, rows, k, fmt):
+    """Random codes on the GPU whose rows are padded to 16 bytes with NaN codes."""
+    room = torch.full((rows, (k + 15) // 16 * 16), 0x7F, dtype=torch.uint8, device=DEV)
+    room[:, :k] = torch.randn(rows, k, generator=gen, device=DEV).mul(8).to(fmt).view(torch.uint8)
+    return room.view(fmt)[:, :k]
+
+
+def operands(m, n, k, fa, fb, tiles):
+    gen = torch.Generator(device=DEV).manual_seed(m + n + k)
+    g = ref.groups(k)
+    a, b = codes(gen, m, k, fa), codes(gen, n, k, fb)
+    sa = torch.rand(g, m, generator=gen, device=DEV) + 0.1
+    return a, sa, b, torch.rand(g, ref.groups(n) if tiles else n, generator=gen, device=DEV) + 0.1
+
+
+# All of the output against 64 bits, computed on the GPU by plain float64 products.
+@pytest.mark.parametrize("shape", gemm_shapes.F32)
+@pytest.mark.parametrize("tiles", [True, False])
+@pytest.mark.parametrize("fa", [E4M3, E5M2])
+@pytest.mark.parametrize("fb", [E4M3, E5M2])
+def test_every_kernel_with_f32_output(fp4q, shape, tiles, fa, fb):
+    print(shape, tiles, fa, fb, flush=True)
+    m, n, k = shape[:3]
+    assert gemm_shapes.plan(m, n, k, True) == shape[3:]
+    ops = operands(m, n, k, fa, fb, tiles)
+    got = fp4q.fp4q_gemm8(*ops, out_dtype=F32)
+    within(got, *ref.gemm(*ops))
+    assert torch.equal(got, fp4q.fp4q_gemm8(*ops, out_dtype=F32))
+    total = torch.randn(m, n, device=DEV)
+    into = total.clone()
+    assert fp4q.fp4q_gemm8(*ops, out=into, accumulate=True) is into
+    assert torch.equal(into, total + got)
+
+
+@pytest.mark.parametrize("shape", gemm_shapes.BF16)
+@pytest.mark.parametrize("tiles", [True, False])
+@pytest.mark.parametrize("fa", [E4M3, E5M2])
+@pytest.mark.parametrize("fb", [E4M3, E5M2])
+def test_every_kernel_with_bf16_output(fp4q, shape, tiles, fa, fb):
+    print(shape, tiles, fa, fb, flush=True)
+    m, n, k = shape[:3]
+    assert gemm_shapes.plan(m, n, k, False) == shape[3:]
+    ops = operands(m, n, k, fa, fb, tiles)
+    got = fp4q.fp4q_gemm8(*ops)
+    check_bf16(got, *ops)
+    assert torch.equal(got, fp4q.fp4q_gemm8(*ops))
+
+
+@pytest.mark.parametrize("f32,shape", [(f32, s) for f32, shapes in ((False, gemm_shapes.BF16), (True, gemm_shapes.F32))
+                                       for s in shapes if s[3] > 32])
+def test_every_kernel_carries_what_is_not_finite(fp4q, f32, shape):
+    """A NaN scale and a NaN code in the last block of K reach their row and column, no others."""
+    m, n, k = shape[:3]
+    a, sa, b, sb = operands(m, n, k, E4M3, E4M3, False)
+    sa[-1, 5] = float("nan")
+    b.view(torch.uint8)[n - 3, k - 1] = 0x7F
+    want = torch.zeros(m, n, dtype=torch.bool, device=DEV)
+    want[5] = True
+    want[:, n - 3] = True
+    got = fp4q.fp4q_gemm8(a, sa, b, sb, out_dtype=F32 if f32 else BF16)
+    assert torch.equal(got.isnan(), want)
+
 
 # every kernel of the product: few rows, and each size of tile
 SIZES = [(5, 300), (40, 300), (1030, 4100), (2047, 4096), (4000, 4096)]
