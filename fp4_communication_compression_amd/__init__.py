@@ -104,6 +104,17 @@ def _stream(stream, device):
     return ctypes.c_void_p(s.cuda_stream)
 
 
+def _run(entry, stream, device, *args) -> None:
+    """Calls a C entry point, its stream argument last, with the tensors' GPU current: a
+    launch on a default stream goes to the current GPU, whichever one the tensors are on."""
+    import torch
+    if torch._C._cuda_getDevice() == device.index:
+        _check(entry(*args, _stream(stream, device)))
+    else:
+        with torch.cuda.device(device):
+            _check(entry(*args, _stream(stream, device)))
+
+
 def _empty(shape, dtype, device, stream):
     """An output tensor allocated for the stream the kernel will run on, so that
     torch's caching allocator does not hand its memory to other work while that
@@ -189,8 +200,8 @@ def fp4q_compress(x, codes=None, micro_scales=None, block_scales=None, flags: in
     if block_scales is None:
         block_scales = _empty((rows, L // 256), torch.float32, dev, stream)
     gpu = _on_gpu(x, *_payload_args(codes, micro_scales, block_scales, rows * L, "output"))
-    _check(lib().fp4q_compress_ex(_ptr(x), rows, L, _ptr(codes), _ptr(micro_scales),
-                                  _ptr(block_scales), flags, _stream(stream, gpu)))
+    _run(lib().fp4q_compress_ex, stream, gpu, _ptr(x), rows, L, _ptr(codes), _ptr(micro_scales),
+         _ptr(block_scales), flags)
     return codes, micro_scales, block_scales
 
 
@@ -213,9 +224,8 @@ def fp4q_decompress(codes, micro_scales, block_scales, out=None, out_dtype=None,
     if out is None:
         out = _empty((rows, L), out_dtype or torch.float32, codes.device, stream)
     gpu = _on_gpu(*pay, _arg(out, "output", rows * L, ("float32", "bfloat16")))
-    _check(lib().fp4q_decompress_ex(_ptr(codes), _ptr(micro_scales), _ptr(block_scales), rows, L,
-                                    _ptr(out), _out_dtype_code(out.dtype), flags,
-                                    _stream(stream, gpu)))
+    _run(lib().fp4q_decompress_ex, stream, gpu, _ptr(codes), _ptr(micro_scales), _ptr(block_scales),
+         rows, L, _ptr(out), _out_dtype_code(out.dtype), flags)
     return out
 
 
@@ -239,9 +249,8 @@ def fp4q_decompress_accumulate(payloads, out=None, out_dtype=None, flags: int = 
     ms = PA(*[p[1].data_ptr() for p in payloads])
     bs = PA(*[p[2].data_ptr() for p in payloads])
     cast = lambda a: ctypes.cast(a, ctypes.POINTER(ctypes.c_void_p))
-    _check(lib().fp4q_decompress_accumulate_ex(k, cast(cs), cast(ms), cast(bs), rows, L,
-                                               _ptr(out), _out_dtype_code(out.dtype), flags,
-                                               _stream(stream, gpu)))
+    _run(lib().fp4q_decompress_accumulate_ex, stream, gpu, k, cast(cs), cast(ms), cast(bs), rows, L,
+         _ptr(out), _out_dtype_code(out.dtype), flags)
     return out
 
 
@@ -278,9 +287,9 @@ def fp4q_reduce_requantize(payloads, codes=None, micro_scales=None, block_scales
     cs = PA(*[p[0].data_ptr() for p in payloads])
     ms = PA(*[p[1].data_ptr() for p in payloads])
     bs = PA(*[p[2].data_ptr() for p in payloads])
-    _check(lib().fp4q_reduce_requantize_ex(
-        k, cast(cs), cast(ms), cast(bs), _ptr(local) if local is not None else None, rows, L,
-        _ptr(codes), _ptr(micro_scales), _ptr(block_scales), flags, _stream(stream, gpu)))
+    _run(lib().fp4q_reduce_requantize_ex, stream, gpu, k, cast(cs), cast(ms), cast(bs),
+         _ptr(local) if local is not None else None, rows, L,
+         _ptr(codes), _ptr(micro_scales), _ptr(block_scales), flags)
     return codes, micro_scales, block_scales
 
 
@@ -295,8 +304,7 @@ def fp4q_compress_mx(x, codes=None, scales=None, flags: int = 0, stream=None):
         scales = _empty((rows, L // 32), torch.uint8, x.device, stream)
     gpu = _on_gpu(x, _arg(codes, "output codes", rows * L // 2, ("uint8",)),
             _arg(scales, "output scales", rows * L // 32, ("uint8",)))
-    _check(lib().fp4q_compress_mx(_ptr(x), rows, L, _ptr(codes), _ptr(scales), flags,
-                                  _stream(stream, gpu)))
+    _run(lib().fp4q_compress_mx, stream, gpu, _ptr(x), rows, L, _ptr(codes), _ptr(scales), flags)
     return codes, scales
 
 
@@ -310,8 +318,8 @@ def fp4q_decompress_mx(codes, scales, out=None, out_dtype=None, flags: int = 0, 
     if out is None:
         out = _empty((rows, L), out_dtype or torch.float32, codes.device, stream)
     gpu = _on_gpu(codes, scales, _arg(out, "output", rows * L, ("float32", "bfloat16")))
-    _check(lib().fp4q_decompress_mx(_ptr(codes), _ptr(scales), rows, L, _ptr(out),
-                                    _out_dtype_code(out.dtype), flags, _stream(stream, gpu)))
+    _run(lib().fp4q_decompress_mx, stream, gpu, _ptr(codes), _ptr(scales), rows, L, _ptr(out),
+         _out_dtype_code(out.dtype), flags)
     return out
 
 

@@ -50,6 +50,9 @@ def _lib() -> ctypes.CDLL:
 # The checks and launches below run once per call of a serving step's smallest
 # operators, whose kernels take a few microseconds: they are written to cost little.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+# A launch on a default stream goes to the current GPU, whichever one the tensors are on:
+# with tensors on another GPU, a function calls itself with that one current.
+_current_gpu = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _launch_stream(stream, index):
@@ -179,7 +182,6 @@ def fp4q_rmsnorm(x, weight, eps: float, residual=None, h=None, want_y: bool = Tr
     dtype, rows, cols = _typed(x, "input")
     kind = x.dtype
     _like(weight, "weight", (cols,), kind)
-    given = h
     if residual is not None:
         _like(residual, "residual", x.shape, kind)
         if h is not None:
@@ -188,7 +190,10 @@ def fp4q_rmsnorm(x, weight, eps: float, residual=None, h=None, want_y: bool = Tr
         raise ValueError("fp4q: h is an output of the sum with a residual")
     if not (want_y or want_codes):
         raise ValueError("fp4q: ask for y, codes or both")
-    gpu = _gpu(x, weight, residual, given)
+    gpu = _gpu(x, weight, residual, h)
+    if _current_gpu() != gpu:
+        with torch.cuda.device(gpu):
+            return fp4q_rmsnorm(x, weight, eps, residual, h, want_y, want_codes, want_rstd, stream)
     if residual is not None and h is None:
         h = _new(x, (rows, cols), kind, stream)
     y = _new(x, (rows, cols), kind, stream) if want_y else None
@@ -216,6 +221,9 @@ def fp4q_rmsnorm_backward(dy, h, weight, rstd, dh=None, stream=None):
     if dh is not None:
         _like(dh, "dh", dy.shape, dy.dtype)
     gpu = _gpu(dy, h, weight, rstd, dh)
+    if _current_gpu() != gpu:
+        with torch.cuda.device(gpu):
+            return fp4q_rmsnorm_backward(dy, h, weight, rstd, dh, stream)
     need = _workspace("fp4q_rmsnorm_backward_workspace", rows, cols)
     dx = _new(dy, (rows, cols), dy.dtype, stream)
     dweight = _new(dy, (cols,), torch.float32, stream)
@@ -248,6 +256,9 @@ def fp4q_quantize8(x, dtype=torch.float8_e4m3fn, tiles: bool = False, straight: 
     if not (straight or transposed):
         raise ValueError("fp4q: ask for straight, transposed or both")
     gpu = _gpu(x)
+    if _current_gpu() != gpu:
+        with torch.cuda.device(gpu):
+            return fp4q_quantize8(x, dtype, tiles, straight, transposed, stream)
     codes = scales = codes_t = scales_t = None
     gr, gc = _groups(rows), _groups(cols)
     if straight:
@@ -291,6 +302,9 @@ def fp4q_gemm8(a, a_scales, b, b_scales, out=None, out_dtype=None, accumulate: b
     if code is None or (accumulate and code != FP4Q_OUT_F32):
         raise TypeError("fp4q: out must be float32%s, got %s" % ("" if accumulate else " or bfloat16", dtype))
     gpu = _gpu(a, a_scales, b, b_scales, out)
+    if _current_gpu() != gpu:
+        with torch.cuda.device(gpu):
+            return fp4q_gemm8(a, a_scales, b, b_scales, out, out_dtype, accumulate, stream)
     flags = (FP4Q_FLAG_TILES if tiles else 0) | (FP4Q_FLAG_ACCUMULATE if accumulate else 0)
     need = _workspace("fp4q_gemm8_workspace", M, N, K, code, flags)
     if out is None:
