@@ -8,11 +8,16 @@ marshal arguments: torch tensors in, device pointers and the current HIP stream
 out.  8-bit codes are float8 tensors whose rows begin at multiples of 16 bytes
 (``stride(0) % 16 == 0``); scales are float32, [ceil(cols / 128), rows], or
 [ceil(cols / 128), ceil(rows / 128)] for 128 x 128 tiles.
+
+Autograd records none of these calls: their outputs require no gradients, and a call
+whose inputs do, where gradients are recorded, warns.  A model calls forward and
+backward functions in a ``torch.autograd.Function`` of its own.
 """
 from __future__ import annotations
 
 import ctypes
 import functools
+import warnings
 from typing import NamedTuple, Optional
 
 import torch
@@ -69,6 +74,13 @@ def _gpu(*tensors):
         if t is not None and t.get_device() != first or first < 0:
             raise ValueError("fp4q: every tensor must be on the same GPU (%s, %s)" % (tensors[0].device, t.device))
     return first
+
+
+def _unrecorded(name):
+    """The warning that a gradient ends here (inputs of `name` require one)."""
+    if torch.is_grad_enabled():
+        warnings.warn("fp4q: autograd does not record %s: its outputs pass no gradient on to its inputs; call it "
+                      "in a torch.autograd.Function, or under torch.no_grad()" % name, stacklevel=3)
 
 
 @functools.lru_cache(maxsize=4096)
@@ -190,9 +202,11 @@ def fp4q_rmsnorm(x, weight, eps: float, residual=None, h=None, want_y: bool = Tr
         raise ValueError("fp4q: h is an output of the sum with a residual")
     if not (want_y or want_codes):
         raise ValueError("fp4q: ask for y, codes or both")
+    if x.requires_grad or weight.requires_grad or (residual is not None and residual.requires_grad):
+        _unrecorded("fp4q_rmsnorm")
     gpu = _gpu(x, weight, residual, h)
     if _current_gpu() != gpu:
-        with torch.cuda.device(gpu):
+        with torch.cuda.device(gpu), torch.no_grad():
             return fp4q_rmsnorm(x, weight, eps, residual, h, want_y, want_codes, want_rstd, stream)
     if residual is not None and h is None:
         h = _new(x, (rows, cols), kind, stream)
@@ -220,9 +234,11 @@ def fp4q_rmsnorm_backward(dy, h, weight, rstd, dh=None, stream=None):
     _like(rstd, "rstd", (rows,), torch.float32)
     if dh is not None:
         _like(dh, "dh", dy.shape, dy.dtype)
+    if dy.requires_grad or h.requires_grad or weight.requires_grad or (dh is not None and dh.requires_grad):
+        _unrecorded("fp4q_rmsnorm_backward")
     gpu = _gpu(dy, h, weight, rstd, dh)
     if _current_gpu() != gpu:
-        with torch.cuda.device(gpu):
+        with torch.cuda.device(gpu), torch.no_grad():
             return fp4q_rmsnorm_backward(dy, h, weight, rstd, dh, stream)
     need = _workspace("fp4q_rmsnorm_backward_workspace", rows, cols)
     dx = _new(dy, (rows, cols), dy.dtype, stream)
@@ -255,9 +271,11 @@ def fp4q_quantize8(x, dtype=torch.float8_e4m3fn, tiles: bool = False, straight: 
         raise TypeError("fp4q: codes are float8_e4m3fn or float8_e5m2, not %s" % (dtype,))
     if not (straight or transposed):
         raise ValueError("fp4q: ask for straight, transposed or both")
+    if x.requires_grad:
+        _unrecorded("fp4q_quantize8")
     gpu = _gpu(x)
     if _current_gpu() != gpu:
-        with torch.cuda.device(gpu):
+        with torch.cuda.device(gpu), torch.no_grad():
             return fp4q_quantize8(x, dtype, tiles, straight, transposed, stream)
     codes = scales = codes_t = scales_t = None
     gr, gc = _groups(rows), _groups(cols)
@@ -301,9 +319,11 @@ def fp4q_gemm8(a, a_scales, b, b_scales, out=None, out_dtype=None, accumulate: b
     code = _TYPES.get(dtype)
     if code is None or (accumulate and code != FP4Q_OUT_F32):
         raise TypeError("fp4q: out must be float32%s, got %s" % ("" if accumulate else " or bfloat16", dtype))
+    if a.requires_grad or a_scales.requires_grad or b.requires_grad or b_scales.requires_grad:
+        _unrecorded("fp4q_gemm8")
     gpu = _gpu(a, a_scales, b, b_scales, out)
     if _current_gpu() != gpu:
-        with torch.cuda.device(gpu):
+        with torch.cuda.device(gpu), torch.no_grad():
             return fp4q_gemm8(a, a_scales, b, b_scales, out, out_dtype, accumulate, stream)
     flags = (FP4Q_FLAG_TILES if tiles else 0) | (FP4Q_FLAG_ACCUMULATE if accumulate else 0)
     need = _workspace("fp4q_gemm8_workspace", M, N, K, code, flags)
