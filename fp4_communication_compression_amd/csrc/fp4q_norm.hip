@@ -7,7 +7,8 @@
 //
 // About ten operations per element against 6 to 8 bytes: bound by HBM.  Every
 // tensor is read once and written once: a row stays in the registers of the
-// wavefronts that share it from its load to its last store.
+// wavefronts that share it from its load to its last store.  (The widest fp32 rows
+// that go this way do not fit: where, and what it costs, stands at the kernels.)
 #include "fp4q_f8.h"
 
 namespace {
@@ -50,7 +51,10 @@ struct NormArgs {
 // 16-byte chunks; otherwise chunks lie at any element and the last one may be shorter.
 // 8192 x 4096 bf16 with residual, y and codes: 54.6 us, 5.5 TB/s (a copy reaches 5.2); four
 // wavefronts a row there: with eight it takes 57.5 us, with one (no barrier, 8 chunks a lane)
-// 60.7.  999 x 5003 fp32: 12 us; one row of 4096: 4.7 us.
+// 60.7.  999 x 5003 fp32: 12 us; one row of 4096: 4.7 us.  With fp32 rows of 32769 to 65536
+// 43 words a lane go to scratch memory and back (116 when rows are not whole): 512 x 65536
+// with residual, y and codes takes 140 us (4.1 TB/s; 1024 x 32768 130 us, bf16 of 512 x 65536
+// 58 us and 5.2 TB/s), 512 x 40001 111 us (3.1 TB/s).
 template <typename T, int kWaves, int kChunks, bool kWhole>
 __global__ __launch_bounds__(kWaves == 1 ? 256 : kWaves * kWave) void norm_kernel(NormArgs a) {
     constexpr int kRows = kWaves == 1 ? 4 : 1;
@@ -202,7 +206,10 @@ struct GradArgs {
 // its columns' part of dw in registers over all its rows; a workgroup's teams add theirs
 // through LDS at the end, and weight_grad_kernel adds the workgroups'.  8192 x 4096 bf16 with
 // dh: 54.7 us with the sum of the parts, 4.9 TB/s; a workgroup for each of 1024 rows at a
-// time, without the loads ahead and with four times the parts, took 72 us.
+// time, without the loads ahead and with four times the parts, took 72 us.  With fp32 rows of
+// 8193 to 16384 23 words a lane go to scratch memory and back in every turn (13 when rows are
+// not whole): 2048 x 16384 with dh takes 137 us (3.9 TB/s; bf16 56 us and 4.8 TB/s),
+// 1000 x 16384 80 us (3.3 TB/s).
 template <typename T, int kTeams, int kWaves, int kChunks, bool kWhole>
 __global__ __launch_bounds__(kTeams * kWaves * kWave) void norm_grad_kernel(GradArgs a) {
     constexpr bool kAhead = kChunks == 1;  // where the registers allow it
