@@ -12,9 +12,11 @@
 // under two scales of 2^70 is 0, not 0 infinity).  A scale of a row of b is a
 // multiplication after the matrix core.  The scale of a tile of b, one for all of a
 // wavefront's columns, is split: its power of two goes into the matrix core's
-// products, its rest to a's scales, with no work on the sums.  8192 x 11008,
-// K = 4096 takes 361 us so, 408 with a multiplication of the sums (on a card where
-// the product of the scales took 352); 2047 x 4096, K = 11008 92, 106 and 89.
+// products, its rest to a's scales, with no work on the sums: against the product of
+// the scales it takes 2.5 to 4 % longer (8192 x 11008, K = 4096: 361 for 352 us on one
+// card; 2047 x 4096, K = 11008: 92.5 for 89), a multiplication of the sums 16 to 18 %
+// (408 and 106).  Two forms of a step, the plain one for blocks whose scales allow it,
+// spill hundreds of registers.
 //
 // Two ways to the block's sum:
 //   8-bit matrix core  (bf16 output) one v_mfma_f32_16x16x128_f8f6f4 covers the
@@ -486,10 +488,15 @@ struct Tile {
 };
 
 // Two blocks in LDS: one is multiplied while the next one's loads are under way.
-// 8192 x 11008, K = 4096, E4M3 to bf16: 350 us (2113 TFLOP/s); 8192 x 8192 x 8192: 458 to
-// 508 us (2400 to 2160) from card to card, at which the schedule's details no longer show:
-// the clock under the matrix cores sets it.  11008 x 4096, K = 4001, rows of 128, fp32
-// output: 369 us (977 TFLOP/s).  2047 x 4096, K = 11008: 98 us (1890 TFLOP/s).
+// Over cards, 8192 x 11008, K = 4096, E4M3 to bf16 takes 361 to 378 us (2046 to 1954
+// TFLOP/s), 8192 x 8192 x 8192 480 to 507 (2290 to 2169), 2047 x 4096, K = 11008 92 to 97
+// (2007 to 1903) and 11008 x 4096, K = 4001, rows of 128, fp32 output 375 to 400 (962 to
+// 902).  The matrix cores are busy for 42 to 44 % of the cycles.  Of the first one's 371 us
+// on one card a copy of the loop takes 280 without its loads, 321 without its LDS reads, 321
+// without the scaled additions and 242 without loads and reads; of the last one's 400 us
+// 290, 342, 330 and 273.  So no one part sets the time: they overlap in part, loads least
+// of all, with one block under way.  256 x 256 tiles with rows of b's scales spill one
+// register.
 template <typename S, int kFmtA, int kFmtB, bool kTiles, bool kPrecise>
 __global__ __launch_bounds__(S::kThreads, 2) void gemm_kernel(GemmArgs p) {
     __shared__ Stage<S> even;
@@ -542,7 +549,8 @@ __global__ __launch_bounds__(S::kThreads, 2) void gemm_kernel(GemmArgs p) {
 }
 
 // Adds the runs' sums in their order, four neighbours a thread: 48 x 11008 in 4 runs 4 us
-// (8.5 MB), 4096 x 4096 in 2 runs 32 us, about 8 TB/s of the last-level cache.
+// (8.5 MB read), 4096 x 4096 in 2 runs 29 us with fp32 and 25 with bf16 output (134 MB read,
+// 67 or 34 written: 6.9 and 6.8 TB/s, out of the last-level cache in part).
 constexpr int kJoinThreads = 256;
 template <typename Out>
 __global__ __launch_bounds__(kJoinThreads) void join_kernel(const float *partial, int64_t part_size, int parts,
@@ -591,9 +599,9 @@ __device__ __forceinline__ u32x4 load_chunk(const uint8_t *row, int k, int K) {
 // from memory into registers, kAhead blocks' loads at a time.  A load takes 64 neighbouring
 // bytes of each of 16 rows (with a lane's 32 bytes side by side, 16 bytes at every 32, it
 // took a tenth longer).  The parts of the sum are joined through LDS in the wavefronts'
-// order.  4096 x 11008 codes read from HBM take 13 us (3.5 TB/s), 32768 x 4096 33 us
-// (4.1 TB/s, with two workgroups on a CU: at most 64 registers; 37 us with one), for 1 to
-// 16 rows of a.
+// order.  4096 x 11008 codes that come from HBM take 12.2 us with one row of a (3.7 TB/s; 9.5
+// out of the last-level cache), 14.5 with 16 rows; 32768 x 4096 33 us (4.1 TB/s, with two
+// workgroups on a CU: at most 64 registers; 37 us with one).
 constexpr int kStripWaves = 16, kAhead = 4, kStripThreads = kStripWaves * kWave;
 template <int kFmtA, int kFmtB, bool kTiles, bool kPrecise>
 __global__ __launch_bounds__(kStripThreads, kTiles && !kPrecise ? 8 : 4) void strip_kernel(GemmArgs p) {

@@ -23,12 +23,12 @@ struct Plan {
 // three workgroups on a CU and its beginning and end cost start_us besides: fitted to the
 // times of every tile with 1 to 16 runs over 44 products (17 x 4096 to 8192 x 4096, K from
 // 1000 to 16384, both output types; over these the choice takes 1.6 % longer than the best
-// way on average, 20 % at most).  So large tiles serve large outputs (8192 x 11008,
-// K = 4096: 376 us in 256 x 256 tiles, 419 us in 128 x 128) and small ones fill the card
-// when the output is small (1000 x 4096, K = 4096: 25.5 us in 64 x 128 tiles, 39 us in
-// 256 x 256).  Cutting K fills it further, for a second launch and one write and read of
-// every run's sums (17 x 4096, K = 4096: 10.2 us in 6 runs, 12.7 in 16, 19 in one;
-// 2047 x 4096, K = 11008: 101 us in 256 x 256 tiles with 2 runs, 92 us in 128 x 128 with one).
+// way on average, 20 % at most; over 24 others, drawn at random, 2.0 % and 14 %).  So large
+// tiles serve large outputs (the GPU's own time on one card for 8192 x 11008, K = 4096:
+// 359 us in 256 x 256 tiles, 415 in 128 x 128) and small ones fill the card when the output
+// is small (1000 x 4096, K = 4096: 25 us in 64 x 128 tiles, 54 in 256 x 256).  Cutting K
+// fills it further, for a second launch and one write and read of every run's sums
+// (17 x 4096, K = 4096: 10.1 us in 6 runs, 12.4 in 16, 19.1 in one).
 constexpr int kCus = 256;
 inline Plan plan_of(int64_t M, int64_t N, int64_t K, bool precise) {
     Plan plan = {Way::kStrip, kStrip, kStrip, 1, 0, 0};

@@ -5,8 +5,9 @@
 // One pass over the tensor: a workgroup holds a 128 x 128 tile in registers,
 // 8 x 8 elements a thread, finds the maxima it needs and writes both orders of
 // codes.  Bound by HBM: 2 bytes read and 1 or 2 written per bf16 element.
-// 8192 x 4096 bf16: both orders 24.9 us (5.4 TB/s), rows alone 17.3 us (5.9 TB/s);
-// 11008 x 4096 tiles in both orders 31.8 us (5.7 TB/s).
+// 8192 x 4096 bf16: both orders 25.0 us (5.4 TB/s), rows alone 17.3 us (5.9 TB/s);
+// fp32: 41.7 us (4.8 TB/s) and 31.1 us (5.4 TB/s), tiles in both orders 38.7 us (5.2 TB/s).
+// 11008 x 4096 bf16, tiles in both orders: 32.3 us (5.6 TB/s).
 #include "fp4q_f8.h"
 
 namespace {
