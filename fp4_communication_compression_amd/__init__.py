@@ -325,13 +325,19 @@ def fp4q_decompress_mx(codes, scales, out=None, out_dtype=None, flags: int = 0, 
 
 _LINEAR = ("FP4Q_GROUP8", "FP4Q_E4M3", "FP4Q_E5M2", "FP4Q_FLAG_TILES", "FP4Q_FLAG_ACCUMULATE", "RmsNorm",
            "Quantized8", "fp4q_rmsnorm", "fp4q_rmsnorm_backward", "fp4q_quantize8", "fp4q_gemm8")
+_GATED = ("FP4Q_ACT_SILU", "FP4Q_ACT_GELU", "FP4Q_ACT_GELU_TANH", "FP4Q_ACT_RELU", "Gated8", "Gated8Grad",
+          "fp4q_gated8", "fp4q_gated8_backward", "fp4q_gemv4", "fp4q_gated4")
 
 
 def __getattr__(name):
-    """The 8-bit linear-layer operators, from their module at first use: it imports
+    """The linear-layer and gated operators, from their modules at first use: they import
     torch, which the package itself leaves to the calls."""
     if name in _LINEAR:
         from . import linear
         globals().update({n: getattr(linear, n) for n in _LINEAR})
+        return globals()[name]
+    if name in _GATED:
+        from . import gated
+        globals().update({n: getattr(gated, n) for n in _GATED})
         return globals()[name]
     raise AttributeError("module %r has no attribute %r" % (__name__, name))

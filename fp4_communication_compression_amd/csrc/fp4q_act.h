@@ -1,0 +1,79 @@
+// fp4q_act.h -- the gated operators' activation functions and their derivatives, in fp32.
+//
+//   silu       g p(g)                                 p the logistic function
+//   gelu       g P(g)                                 P the normal distribution's: erfc(-g / sqrt 2) / 2
+//   gelu_tanh  g (1 + tanh(c (g + d g^3))) / 2 = g p(2 c (g + d g^3)),   c = sqrt(2 / pi), d = 0.044715
+//   relu       max(g, 0), with derivative 0 at 0
+//
+// With e = exp(-z), p(z) = 1 / (1 + e) and 1 - p(z) = e p(z), so the derivative p (1 - p) has
+// no cancellation.  z is held to [-kFar, kFar]: beyond it p is 0 or 1 to 2^-115, and e stays
+// finite (0 infinity would be NaN).  A NaN stays NaN: the limits are taken by comparisons.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include "fp4q_gated.h"
+
+namespace fp4q_act {
+
+constexpr float kFar = 80.0f;
+
+// e^z: 2^t of the rounded t = z log2(e), then the rest of the product (the rounding's error
+// and log2(e)'s bits below fp32) to first order: without it an error of |z| 2^-24.
+__device__ __forceinline__ float exp_of(float z) {
+    constexpr float kLog2e = 1.44269504088896340736f, kLog2eLow = (float)(1.44269504088896340736 - (double)kLog2e);
+    constexpr float kLn2 = 0.693147180559945309417f;
+    const float t = z * kLog2e, rest = fmaf(z, kLog2eLow, fmaf(z, kLog2e, -t));
+    const float e = __builtin_amdgcn_exp2f(t);
+    return fmaf(e, rest * kLn2, e);
+}
+
+struct Logistic {
+    float p, q;  // p(z), 1 - p(z)
+};
+__device__ __forceinline__ Logistic logistic(float z) {
+    z = z > kFar ? kFar : z < -kFar ? -kFar : z;
+    const float e = exp_of(-z), p = __builtin_amdgcn_rcpf(1.0f + e);
+    return {p, e * p};
+}
+
+struct Value {
+    float act, slope;
+};
+// The activation and its derivative; what is not used is not computed.
+template <int kAct>
+__device__ __forceinline__ Value activate(float g) {
+    if constexpr (kAct == FP4Q_ACT_SILU) {
+        const Logistic s = logistic(g);
+        return {g * s.p, fmaf(g * s.p, s.q, s.p)};
+    } else if constexpr (kAct == FP4Q_ACT_GELU) {
+        const float cdf = 0.5f * erfcf(g * -0.70710678118654752440f);
+        // exp(-g^2 / 2): beyond 2 * kFar nothing that g could make count
+        const float h = 0.5f * g * g;
+        const float density = h > kFar ? 0.0f : 0.39894228040143267794f * exp_of(-h);
+        return {g * cdf, fmaf(g, density, cdf)};
+    } else if constexpr (kAct == FP4Q_ACT_GELU_TANH) {
+        constexpr float kTwoC = 1.59576912160573071176f, kD = 0.044715f;
+        // |g| > 16 gives |z| > kFar; the square of a larger one could leave fp32's range
+        const float near = g > 16.0f ? 16.0f : g < -16.0f ? -16.0f : g, square = near * near;
+        const Logistic s = logistic(kTwoC * near * fmaf(kD, square, 1.0f));
+        const float slope_z = kTwoC * fmaf(3.0f * kD, square, 1.0f);
+        return {g * s.p, fmaf(near * slope_z * s.p, s.q, s.p)};
+    } else {
+        return {g > 0.0f ? g : g == g ? 0.0f : g, g > 0.0f ? 1.0f : g == g ? 0.0f : g};
+    }
+}
+
+// Calls f(std::integral_constant<int, activation>) for the activation of that number.
+template <typename F>
+__host__ __device__ __forceinline__ auto with_act(int act, F &&f) {
+    switch (act) {
+        case FP4Q_ACT_SILU: return f(std::integral_constant<int, FP4Q_ACT_SILU>{});
+        case FP4Q_ACT_GELU: return f(std::integral_constant<int, FP4Q_ACT_GELU>{});
+        case FP4Q_ACT_GELU_TANH: return f(std::integral_constant<int, FP4Q_ACT_GELU_TANH>{});
+        default: return f(std::integral_constant<int, FP4Q_ACT_RELU>{});
+    }
+}
+inline bool bad_act(int act) { return act < FP4Q_ACT_SILU || act > FP4Q_ACT_RELU; }
+
+}  // namespace fp4q_act
