@@ -4,16 +4,20 @@
 //   out[m][n] = sum over blocks b of 256 of s[n][b] sum over k in b of x[m][k] e[n][k] u[n][k / 16]
 //
 // with E2M1 codes e, E4M3 micro-scales u and fp32 block scales s.  e u has at most 6
-// significant bits, so it is exact in bf16, and so are its products with a bf16 x in the
-// 16-bit matrix core, which adds them in fp32.  An fp32 x (given, or x transformed instead of
-// a transformed weight) is cut into three bf16 parts that sum to it; the parts are rows of
-// their own, three to a row of x, and their sums are added at the end: the matrix core has 16
-// columns anyway, and the time is that of reading the payload.
+// significant bits and lies between 2^-10 and 2688: it is exact in fp16, at one packed
+// conversion and one packed multiplication for two codes.  x becomes fp16 under a power of
+// two for each row and block of 256: for bf16 x that is exact but for what lies 2^-28 below
+// the block's largest value; fp32 x, and x transformed instead of a transformed weight, are
+// cut into two fp16 parts, 22 bits below the largest.  The parts are columns of the matrix
+// core's product like the rows of x, their sums are added at the end: it has 16 columns
+// anyway, and the time is that of reading the payload.  Products are exact and added in fp32.
 #include <hip/hip_runtime.h>
 
 #include <stdint.h>
 
+#include <algorithm>
 #include <type_traits>
+#include <utility>
 
 #include "fp4q_act.h"
 #include "fp4q_f8.h"
@@ -24,34 +28,45 @@ using namespace fp4q_f8;
 using namespace fp4q_act;
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 
-constexpr int kBlock = FP4Q_BLOCK, kStrip = 16, kParts = 3;
+constexpr int kBlock = FP4Q_BLOCK, kStrip = 16;
 
 struct Payload {
     const uint8_t *codes, *micro;
     const float *block;
 };
 struct Gemv4Args {
-    const uint16_t *x;  // [M parts x K] bf16
+    const void *x;      // [M x K] of the given type; or, made ready, [M parts x K] fp16
+    const float *down;  // made ready: what each part's block is to be multiplied by
     Payload w, up;      // up: the gated form's second weight
     void *out;
-    int M, N, K, parts, act, out_f32;
+    int M, N, K, parts, act, out_f32, x_f32, transform;
 };
 
-// ------------------------------------------------------------------ x in parts
-// A wavefront takes a block of 256 of a row, four neighbours a lane: the Walsh-Hadamard
-// transform in fp32 (strides 1 and 2 in a lane, 4 to 128 over the lanes), then three parts of
-// 8 bits each, cut off and not rounded, so that a part never leaves bf16's range.
-template <typename T, bool kTransform>
-__global__ __launch_bounds__(kWave) void parts_kernel(const T *x, uint16_t *parts, int K) {
-    const int lane = threadIdx.x, blocks = K / kBlock;
-    const int64_t row = (int64_t)(blockIdx.x / (unsigned)blocks);
-    const int k = (int)(blockIdx.x % (unsigned)blocks) * kBlock + 4 * lane;
+// ------------------------------------------------------------------ x as fp16
+// A lane's place of columns k .. k + 7 of a block of 256, in units of 8: the matrix core's
+// step (h, j) takes the codes' dword j of a lane's 16 bytes from each half h of the block's
+// 128, so quarter q needs columns 128 h + 32 q + 8 j; they lie at 16 h + 4 j + q.
+__device__ __forceinline__ int place_of(int k) { return (k & 128) | (k & 24) << 2 | (k & 96) >> 2 | (k & 7); }
+
+// A block of 256 of a row, four neighbours a lane of a wavefront.
+struct Rowblock {
     float v[4];
+    __device__ __forceinline__ void load(const float *x) {
+        const f32x4 w = reinterpret_cast<const f32x4 *>(x)[threadIdx.x & (kWave - 1)];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = to_float(x[row * K + k + i]);
-    if constexpr (kTransform) {
+        for (int i = 0; i < 4; ++i) v[i] = w[i];
+    }
+    __device__ __forceinline__ void load(const bf16 *x) {
+        const u32x2 w = reinterpret_cast<const u32x2 *>(x)[threadIdx.x & (kWave - 1)];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = __uint_as_float(i & 1 ? w[i >> 1] & 0xFFFF0000u : w[i >> 1] << 16);
+    }
+    // y = H v / 16 in fp32: strides 1 and 2 in a lane, 4 to 128 over the lanes.
+    __device__ __forceinline__ void transform() {
+        const int lane = threadIdx.x & (kWave - 1);
         const float a = v[0] + v[1], b = v[0] - v[1], c = v[2] + v[3], d = v[2] - v[3];
         v[0] = a + c;
         v[1] = b + d;
@@ -69,167 +84,378 @@ __global__ __launch_bounds__(kWave) void parts_kernel(const T *x, uint16_t *part
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[i] *= 0.0625f;
     }
+    // The parts at to, to + pitch and what brings each back at down, down + down_pitch.  The
+    // largest value comes to 2^14 .. 2^15; the second part holds what the first one's rounding
+    // left, times 2^11.  A block that is not finite keeps its values, which are not either.
+    // (down is 2^-17 of the factor that it stands for: see the product.)
+    __device__ __forceinline__ void store(_Float16 *to, int64_t pitch, float *down, int64_t down_pitch, int parts) {
+        const int lane = threadIdx.x & (kWave - 1);
+        unsigned top = 0;
 #pragma unroll
-    for (int p = 0; p < kParts; ++p) {
-        u32x2 w = {0, 0};
+        for (int i = 0; i < 4; ++i) top = umax(top, mag(v[i]));
+        top = max64(top);
+        const bool finite = top < 0x7F800000u;
+        const int e = finite ? max((int)(top >> 23) - 127, -84) : 14;
+        const float power = __uint_as_float((unsigned)(127 + 14 - e) << 23);
+        if (lane < parts) down[lane * down_pitch] = __uint_as_float((unsigned)(127 - 14 - 17 + e - 11 * lane) << 23);
+        const int at = place_of(4 * lane);
+        for (int p = 0; p < parts; ++p) {
+            f16x2 w[2];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const unsigned high = __float_as_uint(v[i]) & 0xFFFF0000u;
-            w[i >> 1] |= i & 1 ? high : high >> 16;
-            // what is not finite is all in the first part
-            v[i] = mag(v[i]) < 0x7F800000u ? v[i] - __uint_as_float(high) : 0.0f;
+            for (int i = 0; i < 4; ++i) {
+                const float scaled = p ? v[i] : v[i] * power;
+                const _Float16 half = (_Float16)scaled;
+                w[i >> 1][i & 1] = half;
+                v[i] = finite ? (scaled - (float)half) * 2048.0f : 0.0f;
+            }
+            *reinterpret_cast<u32x2 *>(to + p * pitch + at) =
+                u32x2{__builtin_bit_cast(unsigned, w[0]), __builtin_bit_cast(unsigned, w[1])};
         }
-        *reinterpret_cast<u32x2 *>(parts + (row * kParts + p) * K + k) = w;
+    }
+};
+__device__ __forceinline__ Rowblock ready(const Gemv4Args &p, int64_t row, int kb) {
+    Rowblock r;
+    const int64_t from = row * p.K + kb * kBlock;
+    if (p.x_f32)
+        r.load(static_cast<const float *>(p.x) + from);
+    else
+        r.load(static_cast<const bf16 *>(p.x) + from);
+    return r;
+}
+
+// x made ready in memory, for calls whose x does not fit a workgroup's LDS: parts [M parts x
+// K] and factors [M parts x K / 256].
+constexpr int kReadyWaves = 4;
+__global__ __launch_bounds__(kReadyWaves *kWave) void ready_kernel(Gemv4Args p, _Float16 *to, float *down) {
+    const int blocks = p.K / kBlock, kb = (int)blockIdx.x * kReadyWaves + threadIdx.x / kWave;
+    if (kb >= blocks) return;
+    for (int64_t row = blockIdx.y; row < p.M; row += gridDim.y) {
+        Rowblock r = ready(p, row, kb);
+        if (p.transform) r.transform();
+        r.store(to + row * p.parts * p.K + kb * kBlock, p.K, down + row * p.parts * blocks + kb, blocks, p.parts);
     }
 }
 
 // -------------------------------------------------------------------- product
-// What a lane holds of a block of a weight's row: its codes 32 q .. 32 q + 31 and 128 + 32 q
-// .. (a load takes 64 neighbouring bytes of each of 16 rows), their micro-scales and the
-// block scales of the four rows whose sums it gets.
+// A range of rows of one of a payload's arrays, read through a descriptor: rows past the
+// end read as zeros.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_at(const void *base, int first, int rows, int pitch) {
+    const uint64_t at = (uint64_t)base + (uint64_t)((int64_t)first * pitch);
+    // (all of it is uniform, which the compiler does not see in a loop: it would read the
+    // descriptor lane by lane)
+    const unsigned low = (unsigned)__builtin_amdgcn_readfirstlane((int)(unsigned)at);
+    const unsigned high = (unsigned)__builtin_amdgcn_readfirstlane((int)(unsigned)(at >> 32));
+    return __builtin_amdgcn_make_buffer_rsrc((void *)((uint64_t)high << 32 | low), 0,
+                                             __builtin_amdgcn_readfirstlane(rows * pitch), 0x00020000);
+}
+
+// A block of 16 rows of a weight as loaded: whole 128-byte pieces of 8 rows a load (16 rows'
+// 64 bytes, as the matrix core wants them, took 8.0 instead of 5.9 us for 22 MB, without any
+// work on them), a dword of the micro-scales and a row's block scale ...
+struct Fetched {
+    u32x4 codes[2];
+    unsigned micro, scale;
+};
+// ... and as a lane needs it: its row's codes 32 q .. 32 q + 31 and 128 + 32 q .., their
+// micro-scales, and the block scales of the four rows whose sums it gets.
 struct Piece {
     u32x4 codes[2];
     unsigned micro[2];
-    float scale[4];
+    f32x4 scale;
 };
+// Through a part of LDS of the wavefront's own.  Chunk c (16 bytes) of row r lies at chunk
+// c ^ (r / 2 & 7), so that no two lanes of a read meet in a bank; the loads fetch it so.
+struct Turn {
+    u32x4 codes[16 * 8];
+    unsigned micro[64];
+    float scale[16];
+};
+// (other types' views of them, which the compiler has to keep in order with the stores)
+typedef uint16_t AnyHalf __attribute__((may_alias));
+typedef f32x4 AnyQuad __attribute__((may_alias));
 
-// Eight codes times their micro-scale and 2^-11 in bf16: at most 1.32, so that a block's sum
-// with |x| < 2^118 stays finite; the block scale takes the 2^11 back (a finite weight's block
-// scale is below 2^117).
-constexpr float kDown = 0x1p-11f, kUp = 0x1p11f;
-__device__ __forceinline__ bf16x8 weights_of(unsigned codes, float micro) {
-    u32x4 w;
-    auto pair = [&](auto v) {
-        // exact: the low halves are zero
-        return __builtin_amdgcn_perm(__float_as_uint(v[1] * micro), __float_as_uint(v[0] * micro), 0x07060302u);
-    };
-    w[0] = pair(fp4q_num::e2m1_values<0>(codes, kDown));
-    w[1] = pair(fp4q_num::e2m1_values<1>(codes, kDown));
-    w[2] = pair(fp4q_num::e2m1_values<2>(codes, kDown));
-    w[3] = pair(fp4q_num::e2m1_values<3>(codes, kDown));
-    return __builtin_bit_cast(bf16x8, w);
+// Eight codes times their micro-scale.
+__device__ __forceinline__ f16x8 weights_of(unsigned codes, _Float16 micro) {
+    f16x2 w[4] = {fp4q_num::e2m1_halves<0>(codes), fp4q_num::e2m1_halves<1>(codes), fp4q_num::e2m1_halves<2>(codes),
+                  fp4q_num::e2m1_halves<3>(codes)};
+    f16x8 v;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        w[i] *= f16x2{micro, micro};
+        v[2 * i] = w[i][0];
+        v[2 * i + 1] = w[i][1];
+    }
+    return v;
 }
 
-// A workgroup takes 16 rows of the weight (gated: 8 of each) and up to 16 kCols rows of x
-// or of its parts; its wavefronts share K, a block each in turn.
-template <int kWaves, int kCols, bool kGated>
+template <typename F, int... I>
+__device__ __forceinline__ void static_for_impl(F &&f, std::integer_sequence<int, I...>) {
+    (f(std::integral_constant<int, I>{}), ...);
+}
+template <int N, typename F>
+__device__ __forceinline__ void static_for(F &&f) {
+    static_for_impl(f, std::make_integer_sequence<int, N>{});
+}
+
+// Where the matrix core's second operand comes from.
+enum class Source {
+    kStaged,  // the workgroup makes x ready itself, in LDS
+    kOne,     // made ready in memory; a wavefront has one block of K, whose x it holds for all units
+    kMemory,  // made ready in memory, loaded with each block
+};
+
+// A workgroup takes units of the weight in turn, kStrips strips of 16 rows each (gated: 16 rows
+// of the gate and the same of the up projection), for up to 16 kCols rows of x or of its parts.
+// Its wavefronts share K, every kWaves-th block each; loads run kBlocksAhead blocks ahead, into
+// the next unit too.  There are no branches around them: what does not exist is read through an
+// empty descriptor (behind a branch the compiler would wait for all loads under way).
+template <int kWaves, int kCols, int kStrips, int kBlocksAhead, bool kGated, Source kSource>
 __global__ __launch_bounds__(kWaves *kWave) void gemv4_kernel(Gemv4Args p) {
-    __shared__ f32x4 part[kWaves][kCols][kWave];
-    __shared__ float sums[16 * kCols][kStrip + 1];
-    constexpr int kOut = kGated ? kStrip / 2 : kStrip;
+    static_assert(!kGated || kStrips == 2, "a pair");
+    constexpr int kOut = kGated ? kStrip : kStrip * kStrips, kAhead = kBlocksAhead * kStrips;
+    constexpr bool kStage = kSource == Source::kStaged, kRing = kSource == Source::kMemory;
+    extern __shared__ char room[];  // two units' sums; x and its factors
     const int lane = threadIdx.x & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int row16 = lane & 15, quarter = lane >> 4;
-    const int n0 = (int)blockIdx.x * kOut, blocks = p.K / kBlock;
+    const int blocks = p.K / kBlock, units = (p.N + kOut - 1) / kOut, step = (int)gridDim.x;
     const int each = 16 * kCols / p.parts, m0 = (int)blockIdx.y * each;  // rows of x here
-    const int cols = min(each, p.M - m0) * p.parts;
-    // the weight and row behind row r of 16; rows past the end repeat the last one
-    auto row_of = [&](int r) { return (int64_t)min(n0 + r % kOut, p.N - 1); };
-    auto weight_of = [&](int r) -> const Payload & { return kGated && r >= kOut ? p.up : p.w; };
-    const uint8_t *codes = weight_of(row16).codes + row_of(row16) * (p.K / 2) + 16 * quarter;
-    const uint8_t *micro = weight_of(row16).micro + row_of(row16) * (p.K / 16) + 2 * quarter;
-    const float *block = weight_of(4 * quarter).block;
-    const uint16_t *x = p.x + (int64_t)m0 * p.parts * p.K + 32 * quarter;
+    const int rows = min(each, p.M - m0), cols = rows * p.parts;
+    float *sums = reinterpret_cast<float *>(room);  // [2][kWaves][kStrips][cols][16]
+    const int sums_each = kWaves * kStrips * cols * 16;
 
-    f32x4 acc[kCols];
-#pragma unroll
-    for (int c = 0; c < kCols; ++c) acc[c] = f32x4{0, 0, 0, 0};
-    auto load = [&](Piece &w, int kb) {
-        w.codes[0] = *reinterpret_cast<const u32x4 *>(codes + kb * (kBlock / 2));
-        w.codes[1] = *reinterpret_cast<const u32x4 *>(codes + kb * (kBlock / 2) + 64);
-        w.micro[0] = *reinterpret_cast<const uint16_t *>(micro + kb * 16);
-        w.micro[1] = *reinterpret_cast<const uint16_t *>(micro + kb * 16 + 8);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) w.scale[e] = kUp * block[row_of(4 * quarter + e) * blocks + kb];
+    const int code_pitch = p.K / 2, micro_pitch = p.K / 16, block_pitch = 4 * blocks;
+    const int row8 = lane >> 3, chunk = (lane & 7) ^ (row8 >> 1);
+    const int code_at = row8 * code_pitch + 16 * chunk, code_at8 = (row8 + 8) * code_pitch + 16 * (chunk ^ 4);
+    const int micro_at = (lane >> 2) * micro_pitch + 4 * (lane & 3), block_at = row16 * block_pitch;
+    const int turns = (blocks + kWaves - 1) / kWaves;  // blocks of a wavefront, the last one perhaps missing
+    Fetched fetched[kAhead];
+    auto load = [&](Fetched &w, int unit, int turn, int strip) {
+        const Payload &from = kGated && strip ? p.up : p.w;
+        const int n0 = unit * kOut + (kGated ? 0 : strip * kStrip), kb = wave + turn * kWaves;
+        const int here = unit < units && kb < blocks ? max(min(kStrip, p.N - n0), 0) : 0;
+        const auto codes = rows_at(from.codes, n0, here, code_pitch), micro = rows_at(from.micro, n0, here, micro_pitch),
+                   block = rows_at(from.block, n0, here, block_pitch);
+        w.codes[0] = __builtin_amdgcn_raw_buffer_load_b128(codes, code_at, kb * (kBlock / 2), 0);
+        w.codes[1] = __builtin_amdgcn_raw_buffer_load_b128(codes, code_at8, kb * (kBlock / 2), 0);
+        w.micro = __builtin_amdgcn_raw_buffer_load_b32(micro, micro_at, kb * 16, 0);
+        w.scale = __builtin_amdgcn_raw_buffer_load_b32(block, block_at, 4 * kb, 0);
     };
-    auto multiply = [&](const Piece &w, int kb) {
+    Turn &room_here = reinterpret_cast<Turn *>(sums + 2 * sums_each)[wave];
+    auto turned = [&](const Fetched &w) {
+        room_here.codes[lane] = w.codes[0];
+        room_here.codes[64 + lane] = w.codes[1];
+        room_here.micro[lane] = w.micro;
+        room_here.scale[row16] = __uint_as_float(w.scale);
+        Piece t;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            t.codes[h] = room_here.codes[row16 * 8 + ((quarter + 4 * h) ^ (row16 >> 1))];
+            t.micro[h] = reinterpret_cast<const AnyHalf *>(room_here.micro)[row16 * 8 + 4 * h + quarter];
+        }
+        t.scale = reinterpret_cast<const AnyQuad *>(room_here.scale)[quarter];
+        return t;
+    };
+
+    // x: in LDS rows of p.K columns, 16 bytes apart in their banks, then the factors
+    _Float16 *const staged = reinterpret_cast<_Float16 *>(reinterpret_cast<Turn *>(sums + 2 * sums_each) + kWaves);
+    const int pitch = p.K + 8;
+    float *const staged_down = reinterpret_cast<float *>(staged + cols * pitch);
+    struct Part {
+        u32x4 x[kCols][8];
+        float down[kCols];
+    };
+    Part part[kRing ? kBlocksAhead : 1];
+    auto load_x = [&](Part &to, int turn) {
+        const int kb = min(wave + turn * kWaves, blocks - 1);
+#pragma unroll
+        for (int c = 0; c < kCols; ++c) {
+            const int col = min(16 * c + row16, cols - 1);
+            const _Float16 *from;
+            if constexpr (kStage) {
+                from = staged + col * pitch + kb * kBlock;
+                to.down[c] = staged_down[col * blocks + kb];
+            } else {
+                const int64_t row = (int64_t)m0 * p.parts + col;
+                from = static_cast<const _Float16 *>(p.x) + row * p.K + kb * kBlock;
+                to.down[c] = p.down[row * blocks + kb];
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) to.x[c][i] = reinterpret_cast<const u32x4 *>(from)[4 * i + quarter];
+        }
+    };
+    // where the next loads and the next products are
+    int load_unit = (int)blockIdx.x, load_turn = 0, unit = load_unit, turn = 0;
+    auto advance = [&](int &of, int &at) {
+        const bool last = ++at == turns;
+        at = last ? 0 : at;
+        of += last ? step : 0;
+    };
+    auto load_first = [&]() {
+        static_for<kAhead>([&](auto i) {
+            if constexpr (kRing && i.value % kStrips == 0) load_x(part[i.value / kStrips], load_turn);
+            load(fetched[i.value], load_unit, load_turn, i.value % kStrips);
+            if constexpr (i.value % kStrips == kStrips - 1) advance(load_unit, load_turn);
+        });
+    };
+    if constexpr (kStage) {
+        // the loads of x first: a wavefront's loads return in order
+        int at = wave;
+        Rowblock r;
+        r = ready(p, m0 + min(at, rows * blocks - 1) / blocks, min(at, rows * blocks - 1) % blocks);
+        load_first();
+        for (; at < rows * blocks; at += kWaves) {
+            const int row = at / blocks, kb = at % blocks;
+            if (at != wave) r = ready(p, m0 + row, kb);
+            if (p.transform) r.transform();
+            r.store(staged + row * p.parts * pitch + kb * kBlock, pitch, staged_down + row * p.parts * blocks + kb, blocks,
+                    p.parts);
+        }
+        __syncthreads();
+    } else {
+        if constexpr (!kRing) load_x(part[0], 0);
+        load_first();
+    }
+
+    f32x4 acc[kStrips][kCols];
+    auto clear = [&]() {
+#pragma unroll
+        for (int s = 0; s < kStrips; ++s)
+#pragma unroll
+            for (int c = 0; c < kCols; ++c) acc[s][c] = f32x4{0, 0, 0, 0};
+    };
+    clear();
+    auto multiply = [&](const Piece &w, const Part &x, f32x4 (&sum)[kCols]) {
         f32x4 d[kCols];
 #pragma unroll
         for (int c = 0; c < kCols; ++c) d[c] = f32x4{0, 0, 0, 0};
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
+            const f16x2 u = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w.micro[h], 1.0f, false);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float u = i < 2 ? __builtin_amdgcn_cvt_f32_fp8(w.micro[h], 0) : __builtin_amdgcn_cvt_f32_fp8(w.micro[h], 1);
-                const bf16x8 a = weights_of(w.codes[h][i], u);
+            for (int j = 0; j < 4; ++j) {
+                const f16x8 a = weights_of(w.codes[h][j], u[j >> 1]);
 #pragma unroll
-                for (int c = 0; c < kCols; ++c) {
-                    u32x4 b = {0, 0, 0, 0};
-                    const int col = 16 * c + row16;
-                    if (col < cols)
-                        b = *reinterpret_cast<const u32x4 *>(x + (int64_t)col * p.K + kb * kBlock + 128 * h + 8 * i);
-                    d[c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, __builtin_bit_cast(bf16x8, b), d[c], 0, 0, 0);
-                }
+                for (int c = 0; c < kCols; ++c)
+                    d[c] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, __builtin_bit_cast(f16x8, x.x[c][4 * h + j]), d[c], 0, 0, 0);
             }
         }
+        // (d down) 2^17 s: with |x| and the weights below 2^118 both products are finite
 #pragma unroll
         for (int c = 0; c < kCols; ++c)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) acc[c][e] = fmaf(d[c][e], w.scale[e], acc[c][e]);
+            for (int e = 0; e < 4; ++e) sum[c][e] = fmaf(d[c][e] * x.down[c], w.scale[e] * 0x1p17f, sum[c][e]);
     };
-    for (int kb = wave; kb < blocks; kb += kWaves) {
-        Piece w;
-        load(w, kb);
-        multiply(w, kb);
-    }
+    // two units' sums in turn: one meeting a unit keeps writers and readers apart
+    auto finish = [&]() {
 #pragma unroll
-    for (int c = 0; c < kCols; ++c) part[wave][c][lane] = acc[c];
-    __syncthreads();
-    for (int t = threadIdx.x; t < kCols * kWave; t += kWaves * kWave) {
-        const int c = t / kWave, l = t % kWave;
-        f32x4 sum = part[0][c][l];
-#pragma unroll 5
-        for (int w = 1; w < kWaves; ++w) sum += part[w][c][l];
+        for (int s = 0; s < kStrips; ++s)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) sums[16 * c + (l & 15)][4 * (l >> 4) + e] = sum[e];
-    }
-    __syncthreads();
-    const int rows = min(each, p.M - m0);
-    for (int t = threadIdx.x; t < rows * kOut; t += kWaves * kWave) {
-        const int m = t / kOut, n = t % kOut;
-        if (n0 + n >= p.N) continue;
-        float v = 0.0f, u = 0.0f;
-        for (int i = p.parts - 1; i >= 0; --i) {  // the smallest part first
-            v += sums[m * p.parts + i][n];
-            if (kGated) u += sums[m * p.parts + i][n + kOut];
+            for (int c = 0; c < kCols; ++c)
+                if (16 * c + row16 < cols)
+                    *reinterpret_cast<f32x4 *>(sums + ((wave * kStrips + s) * cols + 16 * c + row16) * 16 + 4 * quarter) = acc[s][c];
+        __syncthreads();
+        for (int t = threadIdx.x; t < rows * kOut; t += kWaves * kWave) {
+            const int m = t / kOut, n = t % kOut, strip = kGated ? 0 : n / kStrip;
+            if (unit * kOut + n >= p.N) continue;
+            float v = 0.0f, u = 0.0f;
+            for (int i = 0; i < p.parts; ++i) {
+                const float *from = sums + (strip * cols + m * p.parts + i) * 16 + n % kStrip;
+#pragma unroll
+                for (int w = 0; w < kWaves; ++w) {
+                    v += from[w * kStrips * cols * 16];
+                    if constexpr (kGated) u += from[(w * kStrips + 1) * cols * 16];
+                }
+            }
+            if constexpr (kGated) v = with_act(p.act, [&](auto act) { return activate<act.value>(v).act * u; });
+            const int64_t to = (int64_t)(m0 + m) * p.N + unit * kOut + n;
+            if (p.out_f32)
+                static_cast<float *>(p.out)[to] = v;
+            else
+                static_cast<bf16 *>(p.out)[to] = from_float<bf16>(v);
         }
-        if constexpr (kGated) v = with_act(p.act, [&](auto act) { return activate<act.value>(v).act * u; });
-        const int64_t at = (int64_t)(m0 + m) * p.N + n0 + n;
-        if (p.out_f32)
-            static_cast<float *>(p.out)[at] = v;
-        else
-            static_cast<bf16 *>(p.out)[at] = from_float<bf16>(v);
+        sums = sums == reinterpret_cast<float *>(room) ? sums + sums_each : reinterpret_cast<float *>(room);
+        clear();
+    };
+
+    // whole rounds of the ring: the last one may end with items that do not exist, all zeros
+    const int mine = (units - 1 - (int)blockIdx.x) / step + 1;
+    for (int left = mine * turns; left > 0; left -= kBlocksAhead) {
+        static_for<kAhead>([&](auto i) {
+            constexpr int strip = i.value % kStrips;
+            Part &x = part[kRing ? i.value / kStrips : 0];
+            if constexpr (kStage && strip == 0) load_x(x, turn);
+            multiply(turned(fetched[i.value]), x, acc[strip]);
+            if constexpr (kRing && strip == kStrips - 1) load_x(x, load_turn);
+            load(fetched[i.value], load_unit, load_turn, strip);
+            if constexpr (strip == kStrips - 1) {
+                advance(load_unit, load_turn);
+                if (turn == turns - 1 && unit < units) finish();
+                advance(unit, turn);
+            }
+        });
     }
 }
 
 // ------------------------------------------------------------------------ host
-constexpr int64_t kLimit = kDimLimit / 2;
-
-bool cut(int dtype, uint32_t flags) { return dtype == FP4Q_OUT_F32 || !(flags & FP4Q_FLAG_NO_FWHT); }
+constexpr int64_t kLimit = kDimLimit / 2, kLimitK = (int64_t)1 << 24;
 
 int check_sizes(int64_t M, int64_t K, int dtype, uint32_t flags) {
-    if (M < 0 || K <= 0 || M >= kLimit || K >= kLimit || K % kBlock) return FP4Q_ERR_SHAPE;
+    if (M < 0 || K <= 0 || M >= kLimit || K >= kLimitK || K % kBlock) return FP4Q_ERR_SHAPE;
     if (flags & ~(uint32_t)FP4Q_FLAG_NO_FWHT) return FP4Q_ERR_ARG;
     return dtype == FP4Q_OUT_F32 || dtype == FP4Q_OUT_BF16 ? FP4Q_OK : FP4Q_ERR_ARG;
 }
+int parts_of(int dtype, uint32_t flags) { return dtype == FP4Q_OUT_F32 || !(flags & FP4Q_FLAG_NO_FWHT) ? 2 : 1; }
+
+// Whether every workgroup makes x ready itself, which saves a launch: for as many blocks of
+// 256 of x as its wavefronts do while the weight's first loads are on their way (one row of
+// 11008: 10.3 us instead of 13.5; 4 rows of 4096: 18.0 instead of 20.5 with two payloads of
+// 11008 rows; 5 transformed rows of 4096, 80 blocks: 27.7 instead of 11.9).
+constexpr int kStageBlocks = 64, kStageLds = 64 * 1024;
+int64_t staged_bytes(int64_t cols, int64_t K) { return cols * (2 * (K + 8) + 4 * (K / kBlock)); }
+bool staged(int64_t M, int64_t K, int parts) {
+    return M * parts <= 16 && M * (K / kBlock) <= kStageBlocks && staged_bytes(M * parts, K) <= kStageLds;
+}
 size_t workspace_of(int64_t M, int64_t K, int dtype, uint32_t flags) {
-    return cut(dtype, flags) ? (size_t)(2 * kParts * M * K) : 0;
+    const int parts = parts_of(dtype, flags);
+    return staged(M, K, parts) ? 0 : (size_t)(M * parts * (2 * K + 4 * (K / kBlock)));
 }
 
-template <int kWaves, int kCols, bool kGated>
-int run_kernel(Gemv4Args &p, void *stream) {
+template <int kWaves, int kCols, int kStrips, int kBlocksAhead, bool kGated, Source kSource>
+int run_kernel(Gemv4Args &p, int most, void *stream) {
     const int each = 16 * kCols / p.parts;
     void *args[] = {&p};
-    const dim3 grid((unsigned)ceil_div(p.N, kGated ? kStrip / 2 : kStrip), (unsigned)ceil_div(p.M, each));
-    if (grid.y > 65535u) return FP4Q_ERR_SHAPE;
-    return launch((const void *)&gemv4_kernel<kWaves, kCols, kGated>, grid, kWaves * kWave, args, stream);
+    const int64_t units = ceil_div(p.N, kGated ? kStrip : kStrip * kStrips), chunks = ceil_div(p.M, each);
+    const dim3 grid((unsigned)std::min<int64_t>(units, most), (unsigned)chunks);
+    if (chunks > 65535) return FP4Q_ERR_SHAPE;
+    const int64_t cols = std::min<int64_t>(each, p.M) * p.parts;
+    const int64_t lds = kWaves * (2 * kStrips * cols * 64 + (int64_t)sizeof(Turn)) +
+                        (kSource == Source::kStaged ? staged_bytes(p.M * p.parts, p.K) : 0);
+    const hipError_t e = hipLaunchKernel((const void *)&gemv4_kernel<kWaves, kCols, kStrips, kBlocksAhead, kGated, kSource>,
+                                         grid, dim3(kWaves * kWave), args, (size_t)lds, (hipStream_t)stream);
+    return e == hipSuccess ? FP4Q_OK : FP4Q_ERR_LAUNCH;
 }
+// The kernel and the number of its workgroups, one or two a CU.  Measured (us, payloads from
+// HBM; the other way in brackets):
+//   16 wavefronts for one row of long K: 4096 x 11008 10.3 (8 of them: 12.3); 8 for K <= 4096,
+//   which two workgroups a CU then share: 1024 x 1024 3.7 (4.6), 11008 x 4096 gated 13.7 (15.5)
+//   x in registers where 16 wavefronts have a block each: 16 x 32768 x 4096 22.5 (24.9 without
+//   the second block's loads ahead; gated, whose two strips leave no registers for those, 22.2
+//   against 34)
+//   two strips, which share x, for two column tiles: 64 x 4096 x 4096 19.0 (30.8 with one); one
+//   strip, and more workgroups, for one: 16 x 4096 x 11008 21.8 (24.1)
+constexpr int kCus = 256;
 template <bool kGated>
-int run_product(Gemv4Args &p, void *stream) {
-    const int64_t cols = (int64_t)p.M * p.parts;
-    if (p.parts == kParts) return cols <= 15 ? run_kernel<16, 1, kGated>(p, stream) : run_kernel<16, 3, kGated>(p, stream);
-    if (cols <= 16) return run_kernel<16, 1, kGated>(p, stream);
-    return cols <= 32 ? run_kernel<16, 2, kGated>(p, stream) : run_kernel<16, 4, kGated>(p, stream);
+int run_product(Gemv4Args &p, bool stage, void *stream) {
+    constexpr int kS = kGated ? 2 : 1;
+    const int64_t cols = (int64_t)p.M * p.parts, blocks = p.K / kBlock;
+    if (stage) {
+        if (!kGated && blocks > 16) return run_kernel<16, 1, kS, 1, kGated, Source::kStaged>(p, kCus, stream);
+        return run_kernel<8, 1, kS, 1, kGated, Source::kStaged>(p, 2 * kCus, stream);
+    }
+    if (cols <= 16 && blocks <= 16) return run_kernel<16, 1, kS, 3 - kS, kGated, Source::kOne>(p, kCus, stream);
+    if (cols <= 16) return run_kernel<8, 1, kS, 1, kGated, Source::kMemory>(p, kCus, stream);
+    return run_kernel<8, 2, 2, 1, kGated, Source::kMemory>(p, kCus, stream);
 }
 
 int run(const void *x, int dtype, int64_t M, const Payload &w, const Payload *up, int64_t N, int64_t K, int act,
@@ -256,20 +482,20 @@ int run(const void *x, int dtype, int64_t M, const Payload &w, const Payload *up
         ins[3 + 3 * i] = rng(weights[i].block, 4 * N * (K / kBlock));
     }
     if (clash(outs, 2, ins, 7)) return FP4Q_ERR_ARG;
-    Gemv4Args p = {static_cast<const uint16_t *>(x), weights[0], weights[1], out, (int)M, (int)N, (int)K, 1, act,
-                   out_dtype == FP4Q_OUT_F32};
+    const int parts = parts_of(dtype, flags);
+    Gemv4Args p = {x, nullptr, weights[0], weights[1], out, (int)M, (int)N, (int)K, parts, act,
+                   out_dtype == FP4Q_OUT_F32, dtype == FP4Q_OUT_F32, !(flags & FP4Q_FLAG_NO_FWHT)};
     if (need) {
-        p.x = static_cast<const uint16_t *>(workspace);
-        p.parts = kParts;
-        const bool f32 = dtype == FP4Q_OUT_F32, transform = !(flags & FP4Q_FLAG_NO_FWHT);
-        const void *fn = f32 ? (transform ? (const void *)&parts_kernel<float, true> : (const void *)&parts_kernel<float, false>)
-                             : (const void *)&parts_kernel<bf16, true>;
-        void *args[] = {&x, &workspace, &p.K};
-        if (M * (K / kBlock) > (int64_t)0x7FFFFFFF) return FP4Q_ERR_SHAPE;
-        const int done = launch(fn, dim3((unsigned)(M * (K / kBlock))), kWave, args, stream);
+        _Float16 *to = static_cast<_Float16 *>(workspace);
+        float *down = reinterpret_cast<float *>(to + M * parts * K);
+        void *args[] = {&p, &to, &down};
+        const dim3 grid((unsigned)ceil_div(K / kBlock, kReadyWaves), (unsigned)std::min<int64_t>(M, 65535));
+        const int done = launch((const void *)&ready_kernel, grid, kReadyWaves * kWave, args, stream);
         if (done != FP4Q_OK) return done;
+        p.x = to;
+        p.down = down;
     }
-    return up ? run_product<true>(p, stream) : run_product<false>(p, stream);
+    return up ? run_product<true>(p, !need, stream) : run_product<false>(p, !need, stream);
 }
 
 }  // namespace

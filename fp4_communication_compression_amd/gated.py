@@ -207,7 +207,7 @@ def fp4q_gemv4(x, weight, flags: int = 0, out=None, out_dtype=None, stream=None)
         with torch.cuda.device(gpu), torch.no_grad():
             return fp4q_gemv4(x, weight, flags, out, out_dtype, stream)
     L = _bound or _lib()
-    need = 0 if kind == FP4Q_OUT_BF16 and flags else _linear._workspace("fp4q_gemv4_workspace", M, K, kind, flags)
+    need = _linear._workspace("fp4q_gemv4_workspace", M, K, kind, flags)
     if out is None:
         out = _new(x, (M, N), dtype, stream)
     space = _new(x, (need,), torch.uint8, stream) if need else None
@@ -236,7 +236,7 @@ def fp4q_gated4(x, gate, up, activation: str = "silu", flags: int = 0, out=None,
         with torch.cuda.device(gpu), torch.no_grad():
             return fp4q_gated4(x, gate, up, activation, flags, out, out_dtype, stream)
     L = _bound or _lib()
-    need = 0 if kind == FP4Q_OUT_BF16 and flags else _linear._workspace("fp4q_gemv4_workspace", M, K, kind, flags)
+    need = _linear._workspace("fp4q_gemv4_workspace", M, K, kind, flags)
     if out is None:
         out = _new(x, (M, N), dtype, stream)
     space = _new(x, (need,), torch.uint8, stream) if need else None

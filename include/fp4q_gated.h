@@ -87,14 +87,16 @@ int fp4q_gated8_backward(const void *dy, const void *gate, const void *up, int64
  *               H Q / 16 in each block of 256, and x is transformed instead: H is symmetric,
  *               so x W^T = (x H / 16) Q^T.
  *   out         [M x N] of out_dtype
- *   workspace   fp4q_gemv4_workspace bytes of scratch memory (NULL if 0): for fp32 x and for
- *               transformed payloads, x as three bf16 parts that sum to it exactly
- * The codes times their micro-scales are exact in bf16; their products with x are exact and
- * added in fp32 by the 16-bit matrix core, a block's sum times its scale in fp32.  As for
- * fp4q_compress, x must be finite with |x| < 2^118, which is not checked (a row of x that is
- * not gives a row of out that is not); of a block's sum, what lies below 2^-126 before the
- * scale (times 2^11) and parts of x below 2^-126 may be dropped.
- * 0 <= M, N; 0 < K; all < 2^27. */
+ *   workspace   fp4q_gemv4_workspace bytes of scratch memory (NULL if 0)
+ * The codes times their micro-scales are exact in fp16.  x becomes fp16 under a power of two
+ * (2^98 at most) for each row and block of 256: bf16 x exactly, but for values 2^-28 below
+ * the block's largest; fp32 or transformed x in two parts, to 2^-22 of each value (and
+ * 2^-39 of the block's largest).  Products are exact and added in fp32 by the matrix core, a
+ * block's sum times its scale in fp32.  As for fp4q_compress, x must be finite with
+ * |x| < 2^118, which is not checked (a row of x that is not gives a row of out that is not);
+ * of x what lies below 2^-112, and of a block's sum what lies below 2^-126 before its scale
+ * (times 2^17), may be dropped.
+ * 0 <= M, N < 2^27, 0 < K < 2^24. */
 int fp4q_gemv4_workspace(int64_t M, int64_t K, int dtype, uint32_t flags, size_t *bytes);
 int fp4q_gemv4(const void *x, int dtype, int64_t M, const uint8_t *codes, const uint8_t *micro_scales,
                const float *block_scales, int64_t N, int64_t K, void *out, int out_dtype,

@@ -411,9 +411,9 @@ def test_few_rows_far_from_one(fp4q, scale, plain):
     their range."""
     flags = fp4q.FP4Q_FLAG_NO_FWHT if plain else 0
     w, x = weight(fp4q, 40, 512, flags), rows(3, 512, F32) * scale
-    # parts of x below 2^-126 may be dropped, and of a block's sum as many products, whose
-    # scale is the block's times 2^11
-    low = 512 * 2.0 ** -126 * (float(gref.payload_values(w).abs().max()) + 3 * 2048 * float(w[2].max()))
+    # parts of x below 2^-112 may be dropped (its power of two is at most 2^98), and of a
+    # block's sum what lies below 2^-126 before its scale times 2^17
+    low = 512 * 2.0 ** -112 * float(gref.payload_values(w).abs().max()) + 2 * 2.0 ** -109 * float(w[2].max())
     want, off = gref.gemv4(x, w, not plain)
     within(fp4q.fp4q_gemv4(x.to(DEV), w, flags).cpu(), want, off + low)
     if scale > 1:
