@@ -7,7 +7,7 @@
 //
 // With e = exp(-z), p(z) = 1 / (1 + e) and 1 - p(z) = e p(z), so the derivative p (1 - p) has
 // no cancellation.  z is held to [-kFar, kFar]: beyond it p is 0 or 1 to 2^-115, and e stays
-// finite (0 infinity would be NaN).  A NaN stays NaN: the limits are taken by comparisons.
+// finite (0 infinity would be NaN).  A NaN stays a NaN in every result.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -18,21 +18,16 @@ namespace fp4q_act {
 
 constexpr float kFar = 80.0f;
 
-// e^z: 2^t of the rounded t = z log2(e), then the rest of the product (the rounding's error
-// and log2(e)'s bits below fp32) to first order: without it an error of |z| 2^-24.
-__device__ __forceinline__ float exp_of(float z) {
-    constexpr float kLog2e = 1.44269504088896340736f, kLog2eLow = (float)(1.44269504088896340736 - (double)kLog2e);
-    constexpr float kLn2 = 0.693147180559945309417f;
-    const float t = z * kLog2e, rest = fmaf(z, kLog2eLow, fmaf(z, kLog2e, -t));
-    const float e = __builtin_amdgcn_exp2f(t);
-    return fmaf(e, rest * kLn2, e);
-}
+// e^z as 2^t of the rounded t = z log2(e): off by |z| 2^-24 of itself besides the
+// instruction's own unit (two terms more would take that away, at a tenth of the gradient
+// kernel's time; where |z| is large, e^z or 1 / e^z hardly counts in what is made of it).
+__device__ __forceinline__ float exp_of(float z) { return __builtin_amdgcn_exp2f(z * 1.44269504088896340736f); }
 
 struct Logistic {
     float p, q;  // p(z), 1 - p(z)
 };
 __device__ __forceinline__ Logistic logistic(float z) {
-    z = z > kFar ? kFar : z < -kFar ? -kFar : z;
+    z = __builtin_amdgcn_fmed3f(z, -kFar, kFar);  // (of a NaN -kFar: the callers' products with g keep it)
     const float e = exp_of(-z), p = __builtin_amdgcn_rcpf(1.0f + e);
     return {p, e * p};
 }

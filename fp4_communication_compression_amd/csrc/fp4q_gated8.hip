@@ -83,89 +83,174 @@ __global__ __launch_bounds__(kJoinThreads) void gated_join_kernel(GatedArgs p) {
     store4(static_cast<bf16 *>(p.out) + at, g, left);
 }
 
-// Up to 16 rows of a: the time is that of reading w once.  A workgroup takes 8 rows of the
-// gate and the same 8 of the up projection as the matrix core's 16; its wavefronts share K,
-// each taking every kWaves-th block, whole fragments straight from memory into registers,
-// kAhead blocks' loads at a time.  The parts of the sum are joined through LDS in the
-// wavefronts' order; lanes l and l + 32 hold an output's g and u.
-constexpr int kStripWaves = 16, kAhead = 4, kStripThreads = kStripWaves * kWave, kStripOut = 8;
-template <int kFmtA, int kFmtW>
-__global__ __launch_bounds__(kStripThreads, 4) void gated_strip_kernel(GatedArgs p) {
-    __shared__ f32x4 part[kStripWaves][kWave];
+// Few rows of a: the time is that of reading w once.  A workgroup takes units of 16 outputs in
+// turn: 16 rows of the gate and the same 16 of the up projection, as two strips, for up to
+// 16 kCols rows of a.  Its wavefronts share K, every kWaves-th block of 128 each; the next
+// block's loads, or the next unit's, are under way while one is multiplied.  There are no
+// branches around loads: what does not exist is read through an empty descriptor (behind a
+// branch the compiler would wait for all loads under way).  A load takes the whole 128 bytes
+// of 8 rows; they go through a part of LDS of the wavefront's own to the matrix core's rows.
+constexpr int kStripOut = 16;
+
+// `rows` rows of `pitch` bytes at `base`, the last one to be read up to `wide` bytes.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_at(const uint8_t *base, int64_t first, int rows, int pitch, int wide) {
+    const uint64_t at = (uint64_t)base + (uint64_t)(first * pitch);
+    // (all of it is uniform, which the compiler does not see in a loop)
+    const unsigned low = (unsigned)__builtin_amdgcn_readfirstlane((int)(unsigned)at);
+    const unsigned high = (unsigned)__builtin_amdgcn_readfirstlane((int)(unsigned)(at >> 32));
+    return __builtin_amdgcn_make_buffer_rsrc((void *)((uint64_t)high << 32 | low), 0,
+                                             __builtin_amdgcn_readfirstlane(rows > 0 ? (rows - 1) * pitch + wide : 0),
+                                             0x00020000);
+}
+// 16 bytes of which the first `keep` count.
+__device__ __forceinline__ u32x4 keep_bytes(u32x4 w, int keep) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int k = keep - 4 * i;
+        w[i] = k >= 4 ? w[i] : k <= 0 ? 0u : w[i] & ((1u << (8 * k)) - 1);
+    }
+    return w;
+}
+
+template <int kFmtA, int kFmtW, int kWaves, int kCols>
+__global__ __launch_bounds__(kWaves *kWave) void gated_strip_kernel(GatedArgs p) {
+    __shared__ u32x4 turn[kWaves][16 * 8];  // chunk c of row r at chunk c ^ (r / 2 & 7)
+    extern __shared__ float sums_room[];         // two units' [kWaves][2][M][16]
     const int lane = threadIdx.x & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int row16 = lane & 15, quarter = lane >> 4;
-    const int n0 = (int)blockIdx.x * kStripOut;  // within one tile of scales of either half
-    const int blocks = (p.K + kGroup - 1) / kGroup, whole = p.K / kGroup;
-    const int tiles = 2 * (p.second / kGroup);
-    // rows past the end repeat the last one
-    const int m = min(row16, p.M - 1), n = min(n0 + (row16 & 7), p.N - 1);
-    const uint8_t *a = p.a, *w = p.b + (int64_t)(n + (row16 < 8 ? 0 : p.second)) * p.b_pitch + 16 * quarter;
-    const unsigned row_a = m * (unsigned)p.a_pitch + 16 * quarter;
-    const int tile = n0 / kGroup + (quarter < 2 ? 0 : p.second / kGroup);
-    f32x4 acc = {0, 0, 0, 0};
+    const int blocks = (p.K + kGroup - 1) / kGroup, turns = (blocks + kWaves - 1) / kWaves;
+    const int units = (p.N + kStripOut - 1) / kStripOut, step = (int)gridDim.x;
+    const int tiles = 2 * (p.second / kGroup), wide = (p.K + 15) & ~15, w_pitch = (int)p.b_pitch, a_pitch = (int)p.a_pitch;
 
-    // kCount blocks from kb0, kStripWaves apart; kWhole: all their codes lie before K
-    auto run = [&](int kb0, auto count_of, auto whole_of) FP4Q_INLINE {
-        constexpr int kCount = count_of.value;
-        constexpr bool kWhole = whole_of.value;
-        Raw ra[kCount], rw[kCount];
-        float sa[kCount], s[kCount];
+    float *sums = sums_room;
+    const int sums_each = kWaves * 2 * p.M * 16;
+
+    const int row8 = lane >> 3, chunk = (lane & 7) ^ (row8 >> 1);
+    const int w_at = row8 * w_pitch + 16 * chunk, w_at8 = (row8 + 8) * w_pitch + 16 * (chunk ^ 4);
+    const auto a_rows = rows_at(p.a, 0, p.M, a_pitch, wide);
+    struct Part {  // a block of a
+        Raw codes[kCols];
+        float scale[kCols];
+    };
+    auto load_a = [&](Part &to, int turn_) {
+        const int kb = min(wave + turn_ * kWaves, blocks - 1);
 #pragma unroll
-        for (int i = 0; i < kCount; ++i) {
-            const int kb = kb0 + i * kStripWaves, low = kb * kGroup;
-            if constexpr (kWhole) {
-                rw[i] = {*reinterpret_cast<const u32x4 *>(w + low), *reinterpret_cast<const u32x4 *>(w + low + 64)};
-                ra[i] = {*reinterpret_cast<const u32x4 *>(a + (row_a + low)),
-                         *reinterpret_cast<const u32x4 *>(a + (row_a + low) + 64)};
-            } else {
-                const int left = p.K - 16 * quarter;
-                rw[i] = {load_chunk(w, low, left), load_chunk(w, low + 64, left)};
-                ra[i] = {load_chunk(a + row_a, low, left), load_chunk(a + row_a, low + 64, left)};
-            }
-            sa[i] = p.sa[(int64_t)kb * p.M + m];
-            s[i] = p.sb[(int64_t)kb * tiles + tile];
-        }
-#pragma unroll
-        for (int i = 0; i < kCount; ++i) {
-            Frag<kFmtW, false> first;
-            Frag<kFmtA, false> second;
-            first.set(rw[i]);
-            second.set(ra[i]);
-            const f32x4 d = block_product<false>(first, second, 0);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) acc[e] = fmaf(d[e] * s[i], sa[i], acc[e]);
+        for (int c = 0; c < kCols; ++c) {
+            const int m = min(16 * c + row16, p.M - 1), at = m * a_pitch + 16 * quarter;
+            to.codes[c].low = __builtin_amdgcn_raw_buffer_load_b128(a_rows, at, kb * kGroup, 0);
+            to.codes[c].high = __builtin_amdgcn_raw_buffer_load_b128(a_rows, at + 64, kb * kGroup, 0);
+            to.scale[c] = p.sa[(int64_t)kb * p.M + m];
         }
     };
-    int kb = wave;
-    for (; kb + (kAhead - 1) * kStripWaves < whole; kb += kAhead * kStripWaves)
-        run(kb, std::integral_constant<int, kAhead>{}, std::true_type{});
-    for (; kb + kStripWaves < whole; kb += 2 * kStripWaves) run(kb, std::integral_constant<int, 2>{}, std::true_type{});
-    for (; kb < whole; kb += kStripWaves) run(kb, std::integral_constant<int, 1>{}, std::true_type{});
-    for (; kb < blocks; kb += kStripWaves) run(kb, std::integral_constant<int, 1>{}, std::false_type{});
+    struct Fetched {  // a block of a strip of w
+        u32x4 codes[2];
+        float scale;
+    };
+    auto load_w = [&](Fetched &to, int unit, int turn_, int strip) {
+        const int n0 = unit * kStripOut, kb = wave + turn_ * kWaves;
+        const int here = unit < units && kb < blocks ? min(kStripOut, p.N - n0) : 0;
+        const auto rows = rows_at(p.b, (int64_t)n0 + (strip ? p.second : 0), here, w_pitch, wide);
+        to.codes[0] = __builtin_amdgcn_raw_buffer_load_b128(rows, w_at, kb * kGroup, 0);
+        to.codes[1] = __builtin_amdgcn_raw_buffer_load_b128(rows, w_at8, kb * kGroup, 0);
+        // (an item that does not exist takes any scale: its codes are zeros, but for a NaN's sake its own unit's)
+        const int tile = min(n0, p.N - 1) / kGroup + (strip ? tiles / 2 : 0);
+        to.scale = here > 0 ? p.sb[(int64_t)min(kb, blocks - 1) * tiles + tile] : 0.0f;
+    };
+    int load_unit = (int)blockIdx.x, load_turn = 0, unit = load_unit, turn_now = 0;
+    auto advance = [&](int &of, int &at) {
+        const bool last = ++at == turns;
+        at = last ? 0 : at;
+        of += last ? step : 0;
+    };
+    Part part;
+    Fetched fetched[2];
+    load_a(part, 0);
+    load_w(fetched[0], load_unit, 0, 0);
+    load_w(fetched[1], load_unit, 0, 1);
+    advance(load_unit, load_turn);
 
-    part[wave][lane] = acc;
-    __syncthreads();
-    if (wave > 0 || lane >= 32 || row16 >= p.M) return;
-    f32x4 u = part[0][lane + 32];
-#pragma unroll 3
-    for (int w = 1; w < kStripWaves; ++w) {
-        acc += part[w][lane];
-        u += part[w][lane + 32];
-    }
-    const int first = n0 + 4 * quarter;
-    const int64_t at = (int64_t)row16 * p.N + first;
-    with_act(p.act, [&](auto act) FP4Q_INLINE {
+    f32x4 acc[2][kCols];
+    auto clear = [&]() {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            if (first + e >= p.N) break;
-            if (p.gate) {
-                static_cast<bf16 *>(p.gate)[at + e] = from_float<bf16>(acc[e]);
-                static_cast<bf16 *>(p.up)[at + e] = from_float<bf16>(u[e]);
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+            for (int c = 0; c < kCols; ++c) acc[s][c] = f32x4{0, 0, 0, 0};
+    };
+    clear();
+    // two units' sums in turn: one meeting a unit keeps writers and readers apart
+    auto finish = [&]() {
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+            for (int c = 0; c < kCols; ++c)
+                if (16 * c + row16 < p.M)
+                    *reinterpret_cast<f32x4 *>(sums + ((wave * 2 + s) * p.M + 16 * c + row16) * 16 + 4 * quarter) = acc[s][c];
+        __syncthreads();
+        for (int t = threadIdx.x; t < p.M * kStripOut; t += kWaves * kWave) {
+            const int m = t / kStripOut, n = unit * kStripOut + t % kStripOut;
+            if (n >= p.N) continue;
+            float g = 0.0f, u = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kWaves; ++w) {
+                g += sums[w * 2 * p.M * 16 + t];
+                u += sums[(w * 2 + 1) * p.M * 16 + t];
             }
-            static_cast<bf16 *>(p.out)[at + e] = from_float<bf16>(activate<act.value>(acc[e]).act * u[e]);
+            const int64_t to = (int64_t)m * p.N + n;
+            if (p.gate) {
+                static_cast<bf16 *>(p.gate)[to] = from_float<bf16>(g);
+                static_cast<bf16 *>(p.up)[to] = from_float<bf16>(u);
+            }
+            with_act(p.act, [&](auto act) FP4Q_INLINE { g = activate<act.value>(g).act * u; });
+            static_cast<bf16 *>(p.out)[to] = from_float<bf16>(g);
         }
-    });
+        sums = sums == sums_room ? sums + sums_each : sums_room;
+        clear();
+    };
+
+    const int mine = (units - 1 - (int)blockIdx.x) / step + 1;
+    for (int left = mine * turns; left > 0; --left) {
+        const int kb = wave + turn_now * kWaves, end = p.K - kb * kGroup;  // codes from `end` on do not count
+        if (end < kGroup) {
+#pragma unroll
+            for (int c = 0; c < kCols; ++c) {
+                part.codes[c].low = keep_bytes(part.codes[c].low, end - 16 * quarter);
+                part.codes[c].high = keep_bytes(part.codes[c].high, end - 16 * quarter - 64);
+            }
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                fetched[s].codes[0] = keep_bytes(fetched[s].codes[0], end - 16 * chunk);
+                fetched[s].codes[1] = keep_bytes(fetched[s].codes[1], end - 16 * (chunk ^ 4));
+            }
+        }
+        Frag<kFmtA, false> second[kCols];
+        float sa[kCols];
+#pragma unroll
+        for (int c = 0; c < kCols; ++c) {
+            second[c].set(part.codes[c]);
+            sa[c] = part.scale[c];
+        }
+        load_a(part, load_turn);
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            u32x4 *const mine_here = turn[wave];
+            mine_here[lane] = fetched[s].codes[0];
+            mine_here[64 + lane] = fetched[s].codes[1];
+            const float sw = fetched[s].scale;
+            load_w(fetched[s], load_unit, load_turn, s);
+            Frag<kFmtW, false> first;
+            first.set({mine_here[row16 * 8 + (quarter ^ (row16 >> 1))], mine_here[row16 * 8 + ((quarter + 4) ^ (row16 >> 1))]});
+#pragma unroll
+            for (int c = 0; c < kCols; ++c) {
+                const f32x4 d = block_product<false>(first, second[c], 0);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[s][c][e] = fmaf(d[e] * sw, sa[c], acc[s][c][e]);
+            }
+        }
+        advance(load_unit, load_turn);
+        if (turn_now == turns - 1) finish();
+        advance(unit, turn_now);
+    }
 }
 
 using Large = Shape<2, 4, 8, 4>;   // 256 rows by 128 outputs, a workgroup a CU
@@ -187,9 +272,13 @@ struct Tiled {
     };
     static const void *get(int fa, int fw) { return pick<Kernel>(fa, fw); }
 };
-template <int kFmtA, int kFmtW>
+template <int kWaves, int kCols>
 struct Strip {
-    static const void *get() { return (const void *)&gated_strip_kernel<kFmtA, kFmtW>; }
+    template <int kFmtA, int kFmtW>
+    struct Kernel {
+        static const void *get() { return (const void *)&gated_strip_kernel<kFmtA, kFmtW, kWaves, kCols>; }
+    };
+    static const void *get(int fa, int fw) { return pick<Kernel>(fa, fw); }
 };
 
 constexpr int64_t kLimit = kDimLimit / 2;
@@ -197,9 +286,17 @@ bool bad_gated(int64_t M, int64_t N, int64_t K) {
     return M < 0 || N < 0 || K < 0 || M >= kLimit || N >= kLimit || K >= kLimit ||
            ceil_div(M, 32) * ceil_div(N, 64) > (int64_t)0x7FFFFFFF / 16;
 }
-// The product's plan of the joined rows: tiles of both halves' columns.
+// Strips for up to 16 rows of a, and for up to 64 where every unit has a workgroup and K is
+// short (us, weights from HBM; the tiles' time in brackets: 17 x 2752, K = 4096 9.8 (13.0), 48
+// x 2752, K = 4096 13.2 (16.0), 48 x 1024, K = 1024 5.9 (8.7); with more units a's rows are read
+// too often: 48 x 11008, K = 4096 31.7 (26.1); with long K too: 48 x 2752, K = 11008 28.7
+// (24.3)).  Else the product's plan of the joined rows: tiles of both halves' columns.
 Plan gated_plan(int64_t M, int64_t N, int64_t K) {
-    Plan plan = plan_of(M, 2 * N, K, false);
+    Plan plan = {Way::kStrip, kStrip, kStripOut, 1, 0, 0};
+    const bool few = M <= kStrip || (M <= 64 && N <= kStripOut * kCus && K <= 4096);
+    if (few && K > 0) return plan;
+    // (with K = 0 no strip, which would load a block that is not there; the tiles load none)
+    plan = plan_of(M <= kStrip ? kStrip + 1 : M, 2 * N, K, false);
     plan.tile_n /= 2;
     if (plan.parts > 1) {
         plan.part_size = ceil_div(M * N, 4) * 4;
@@ -251,15 +348,25 @@ int fp4q_gated8(const uint8_t *a, int64_t a_pitch, int a_format, const float *a_
     p.gate = gate;
     p.up = up;
     void *args[] = {&p};
+    if (plan.way == Way::kStrip) {
+        // (M = 64: two units' sums of 8 wavefronts take 128 KiB of LDS)
+        const int waves = M <= 32 ? 16 : 8;
+        const void *fn = M <= 16 ? Strip<16, 1>::get(a_format, w_format)
+                         : M <= 32 ? Strip<16, 2>::get(a_format, w_format) : Strip<8, 4>::get(a_format, w_format);
+        const int64_t units = ceil_div(N, kStripOut);
+        const hipError_t e = hipLaunchKernel(fn, dim3((unsigned)(units < kCus ? units : kCus)), dim3(waves * kWave), args,
+                                             (size_t)(2 * waves * 2 * M * 16 * 4), (hipStream_t)stream);
+        return e == hipSuccess ? FP4Q_OK : FP4Q_ERR_LAUNCH;
+    }
     const void *fn = nullptr;
-    int threads = kStripThreads;
+    int threads = 0;
     auto use = [&](auto shape) {
         using S = decltype(shape);
         fn = Tiled<S>::get(a_format, w_format);
         threads = S::kThreads;
     };
     switch (plan.way) {
-        case Way::kStrip: fn = pick<Strip>(a_format, w_format); break;
+        case Way::kStrip: break;
         case Way::kLow32: use(Low32{}); break;
         case Way::kLow64: use(Low64{}); break;
         case Way::kMedium: use(Medium{}); break;

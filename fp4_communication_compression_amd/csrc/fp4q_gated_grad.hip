@@ -14,8 +14,9 @@ namespace {
 using namespace fp4q_f8;
 using namespace fp4q_act;
 
-constexpr int kThreads = 256;
+constexpr int kRows = 4, kThreads = kGroup / kRows * 16;  // rows of a thread; 8 columns
 constexpr int kWaves = kThreads / kWave;
+enum { kGate, kUp, kY, kTensors };
 
 // One order of codes: rows are the rows of the joined tensor, or its columns.
 struct Codes {
@@ -29,129 +30,139 @@ struct GradArgs {
     int rows, cols, row_tiles, col_tiles;
 };
 
-struct Room {
-    unsigned top[kWaves][kGroup];
-    u32x4 turn[kGroup * kGroup / 16];
-};
+// The largest magnitude of three, NaN if one is: one instruction.
+__device__ __forceinline__ float largest(float a, float b, float c) {
+    return __builtin_elementwise_maximum(__builtin_elementwise_maximum(fabsf(a), fabsf(b)), fabsf(c));
+}
 
 // Codes along the rows of a tile: row r0 + i of `rows`, group `group` of `out`, columns
 // c0 .. c0 + 7 of the tensor of which `left` exist.
 template <int kFmt>
-__device__ __forceinline__ void write_rows(const float (&v)[8][8], const Codes &out, int rows, int r0, int c0, int left,
-                                           int group, int across) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        unsigned top = 0;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) top = umax(top, mag(v[i][j]));
-        const Scale sc = scale_of<kFmt>(max16(top));
-        u32x2 w;
-        w[0] = code_quad<kFmt>(v[i][0], v[i][1], v[i][2], v[i][3], sc);
-        w[1] = code_quad<kFmt>(v[i][4], v[i][5], v[i][6], v[i][7], sc);
-        if (r0 + i >= rows) continue;
-        if (across == 0) out.scales[(int64_t)group * rows + r0 + i] = sc.s;
-        store_bytes8(out.codes + (int64_t)(r0 + i) * out.pitch + c0, left, w);
-    }
+__device__ __forceinline__ void write_row(const float (&v)[8], const Codes &out, int rows, int row, int c0, int left,
+                                          int group, int across) {
+    const float top = largest(largest(largest(v[0], v[1], v[2]), v[3], v[4]), v[5], largest(v[6], v[7], v[7]));
+    const Scale sc = scale_of<kFmt>(max16(mag(top)));
+    u32x2 w;
+    w[0] = code_quad<kFmt>(v[0], v[1], v[2], v[3], sc);
+    w[1] = code_quad<kFmt>(v[4], v[5], v[6], v[7], sc);
+    if (row >= rows) return;
+    if (across == 0) out.scales[(int64_t)group * rows + row] = sc.s;
+    store_bytes8(out.codes + (int64_t)row * out.pitch + c0, left, w);
 }
 
-// Codes along the columns of a tile, turned in LDS: column c of `room` is column first + c of
-// the tensor, of `cols` that exist here, its rows those from row on of `rows`, group `group`.
-template <int kFmt>
-__device__ __forceinline__ void write_cols(const float (&v)[8][8], Room &room, const Codes &out, int64_t all, int first,
-                                           int cols, int row, int rows, int group) {
-    const int t = threadIdx.x, lane = t & (kWave - 1), wave = t / kWave;
-    const int across = t & 15, down = t >> 4;
-    Scale sc[8];
-    unsigned top[8];
+// Thread t holds rows kRows (t / 16) + i and columns 8 (t % 16) + j of the tile.
+template <typename T, int kAct, int kFmt, bool kWhole>
+__global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2) void gated_grad_kernel(GradArgs a) {
+    __shared__ union {
+        unsigned top[kWaves][kTensors][kGroup];           // the wavefronts' largest magnitudes of each column
+        unsigned turn[kTensors][kGroup * kGroup / 4];     // then the columns' codes
+    } room;
+    __shared__ Scale scales[kTensors][kGroup];
+    const int t = threadIdx.x, lane = t & (kWave - 1), wave = t / kWave, across = t & 15, down = t >> 4;
+    const int tc = (int)(blockIdx.x % (unsigned)a.col_tiles), tr = (int)(blockIdx.x / (unsigned)a.col_tiles);
+    const int row = tr * kGroup, col = tc * kGroup, r0 = row + kRows * down, c0 = col + 8 * across;
+    const int64_t from = (int64_t)r0 * a.cols + c0;
+    // the joined tensor: columns N .. P of its first half are zeros, as those of the tile are
+    const int second = a.col_tiles * kGroup;
+    const int64_t joined = (int64_t)second + a.cols;
+
+    float v[kTensors][kRows][8];
+    Eight<T> dy[kRows], gate[kRows], up[kRows];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        top[j] = 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) top[j] = umax(top[j], mag(v[i][j]));
-        top[j] = umax(top[j], (unsigned)__shfl_xor((int)top[j], 16));
-        top[j] = umax(top[j], (unsigned)__shfl_xor((int)top[j], 32));
-        if (lane < 16) room.top[wave][8 * across + j] = top[j];
+    for (int i = 0; i < kRows; ++i) {
+        const int left = r0 + i < a.rows ? a.cols - c0 : 0;
+        const int64_t at = from + (int64_t)i * a.cols;
+        dy[i].template load<kWhole>(static_cast<const T *>(a.dy) + at, left);
+        gate[i].template load<kWhole>(static_cast<const T *>(a.gate) + at, left);
+        up[i].template load<kWhole>(static_cast<const T *>(a.up) + at, left);
     }
-    __syncthreads();  // (also: the last tile's reads of `turn` are done)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
+    for (int i = 0; i < kRows; ++i) {
+        float d[8], g[8], u[8];
+        dy[i].get(d);
+        gate[i].get(g);
+        up[i].get(u);
 #pragma unroll
-        for (int k = 0; k < kWaves; ++k) top[j] = umax(top[j], room.top[k][8 * across + j]);
-        sc[j] = scale_of<kFmt>(top[j]);
-        if (down == 0 && 8 * across + j < cols) out.scales[(int64_t)group * all + first + 8 * across + j] = sc[j].s;
+        for (int j = 0; j < 8; ++j) {
+            const Value f = activate<kAct>(g[j]);
+            v[kGate][i][j] = d[j] * u[j] * f.slope;
+            v[kUp][i][j] = d[j] * f.act;
+            v[kY][i][j] = f.act * u[j];
+        }
+        if (a.along.codes) {
+            write_row<kFmt>(v[kGate][i], a.along, a.rows, r0 + i, c0, 8, tc, across);
+            write_row<kFmt>(v[kUp][i], a.along, a.rows, r0 + i, second + c0, a.cols - c0, a.col_tiles + tc, across);
+        }
     }
-    // column c: 16 slots of 8 bytes (rows 8 s .. 8 s + 7) at slot s ^ (c / 8), so that the 16
-    // lanes of a store meet 16 different slots
-    u32x2 *slots = reinterpret_cast<u32x2 *>(room.turn);
+    if (!a.across.codes && !a.y.codes) return;
+
+    // The columns' largest magnitudes: over a thread's rows, then over the four rows of 16
+    // lanes: an exchange of two registers between rows leaves one's maximum over two rows in
+    // one row and the other's in the other, so that 24 values end as 6 with no lane idle.
+    unsigned top[kTensors * 8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        u32x2 w;
-        w[0] = code_quad<kFmt>(v[0][j], v[1][j], v[2][j], v[3][j], sc[j]);
-        w[1] = code_quad<kFmt>(v[4][j], v[5][j], v[6][j], v[7][j], sc[j]);
-        slots[(8 * across + j) * 16 + (down ^ across)] = w;
+    for (int k = 0; k < kTensors * 8; ++k) {
+        const auto &w = v[k / 8];
+        static_assert(kRows == 4, "four rows");
+        top[k] = mag(largest(largest(w[0][k % 8], w[1][k % 8], w[2][k % 8]), w[3][k % 8], w[3][k % 8]));
+    }
+#pragma unroll
+    for (int k = 0; k < kTensors * 8; k += 4) {
+        const auto p = __builtin_amdgcn_permlane16_swap(top[k], top[k + 1], false, false);
+        const auto q = __builtin_amdgcn_permlane16_swap(top[k + 2], top[k + 3], false, false);
+        const auto r = __builtin_amdgcn_permlane32_swap(umax(p[0], p[1]), umax(q[0], q[1]), false, false);
+        room.top[wave][k / 8][8 * across + k % 8 + (lane >> 4)] = umax(r[0], r[1]);
     }
     __syncthreads();
-    // 8 threads write the 128 bytes of a column
-    const int pair = t & 7;
+    const int cols = min(kGroup, a.cols - col);  // that exist here; of dgate all, zeros too
+    if (t < kTensors * kGroup) {
+        const int which = t / kGroup, c = t % kGroup;
+        unsigned most = room.top[0][which][c];
 #pragma unroll
-    for (int n = 0; n < 4; ++n) {
-        const int c = n * 32 + t / 8, key = c / 8, at = row + 16 * pair;
-        const u32x4 q = room.turn[c * 8 + (pair ^ (key >> 1))];
-        const u32x4 w = key & 1 ? u32x4{q[2], q[3], q[0], q[1]} : q;
-        if (c < cols && at < rows) {
-            uint8_t *p = out.codes + (int64_t)(first + c) * out.pitch + at;
-            if (rows - at >= 16) {
-                __builtin_nontemporal_store(w, reinterpret_cast<u32x4 *>(p));
-            } else {
-                store_bytes8(p, rows - at, u32x2{w[0], w[1]});
-                if (rows - at > 8) store_bytes8(p + 8, rows - at - 8, u32x2{w[2], w[3]});
+        for (int w = 1; w < kWaves; ++w) most = umax(most, room.top[w][which][c]);
+        const Scale sc = which == kY ? scale_of<FP4Q_E4M3>(most) : scale_of<kFmt>(most);
+        scales[which][c] = sc;
+        if (which == kY) {
+            if (a.y.codes && c < cols) a.y.scales[(int64_t)tr * a.cols + col + c] = sc.s;
+        } else if (a.across.codes && (which == kGate || c < cols)) {
+            a.across.scales[tr * joined + (which == kGate ? 0 : second) + col + c] = sc.s;
+        }
+    }
+    __syncthreads();
+    // column c: 32 slots of 4 bytes (rows 4 s .. 4 s + 3) at slot s ^ 2 (c / 8), so that the 64
+    // lanes of a store meet every second bank twice at most
+#pragma unroll
+    for (int k = 0; k < kTensors; ++k)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const Scale sc = scales[k][8 * across + j];
+            room.turn[k][(8 * across + j) * 32 + (down ^ 2 * across)] =
+                k == kY ? code_quad<FP4Q_E4M3>(v[k][0][j], v[k][1][j], v[k][2][j], v[k][3][j], sc)
+                        : code_quad<kFmt>(v[k][0][j], v[k][1][j], v[k][2][j], v[k][3][j], sc);
+        }
+    __syncthreads();
+    // 8 threads write the 128 bytes of a column
+    const int pair = t & 7, at = row + 16 * pair;
+#pragma unroll
+    for (int k = 0; k < kTensors; ++k) {
+        const Codes &out = k == kY ? a.y : a.across;
+        if (!out.codes) continue;
+#pragma unroll
+        for (int n = 0; n < kGroup / (kThreads / 8); ++n) {
+            const int c = n * (kThreads / 8) + t / 8, key = c / 8;
+            const u32x4 q = reinterpret_cast<const u32x4 *>(room.turn[k])[c * 8 + (pair ^ (key >> 1))];
+            const u32x4 w = key & 1 ? u32x4{q[2], q[3], q[0], q[1]} : q;
+            if ((k == kGate || c < cols) && at < a.rows) {
+                uint8_t *p = out.codes + (int64_t)((k == kUp ? second : 0) + col + c) * out.pitch + at;
+                if (a.rows - at >= 16) {
+                    __builtin_nontemporal_store(w, reinterpret_cast<u32x4 *>(p));
+                } else {
+                    store_bytes8(p, a.rows - at, u32x2{w[0], w[1]});
+                    if (a.rows - at > 8) store_bytes8(p + 8, a.rows - at - 8, u32x2{w[2], w[3]});
+                }
             }
         }
     }
-}
-
-// Thread t holds rows 8 (t / 16) + i and columns 8 (t % 16) + j of the tile.
-template <typename T, int kAct, int kFmt, bool kWhole>
-__global__ __launch_bounds__(kThreads) void gated_grad_kernel(GradArgs a) {
-    __shared__ Room room;
-    const int t = threadIdx.x, across = t & 15, down = t >> 4;
-    const int tc = (int)(blockIdx.x % (unsigned)a.col_tiles), tr = (int)(blockIdx.x / (unsigned)a.col_tiles);
-    const int row = tr * kGroup, col = tc * kGroup, r0 = row + 8 * down, c0 = col + 8 * across;
-    const int64_t from = (int64_t)r0 * a.cols + c0;
-
-    float dgate[8][8], dup[8][8], y[8][8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int left = r0 + i < a.rows ? a.cols - c0 : 0;
-        const int64_t at = from + (int64_t)i * a.cols;
-        Eight<T> dy, gate, up;
-        dy.template load<kWhole>(static_cast<const T *>(a.dy) + at, left);
-        gate.template load<kWhole>(static_cast<const T *>(a.gate) + at, left);
-        up.template load<kWhole>(static_cast<const T *>(a.up) + at, left);
-        float d[8], g[8], u[8];
-        dy.get(d);
-        gate.get(g);
-        up.get(u);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const Value v = activate<kAct>(g[j]);
-            dgate[i][j] = d[j] * u[j] * v.slope;
-            dup[i][j] = d[j] * v.act;
-            y[i][j] = v.act * u[j];
-        }
-    }
-    // the joined tensor: columns N .. P of its first half are zeros, as those of the tile are
-    const int second = a.col_tiles * kGroup, cols = min(kGroup, a.cols - col);
-    const int64_t joined = (int64_t)second + a.cols;
-    if (a.along.codes) {
-        write_rows<kFmt>(dgate, a.along, a.rows, r0, c0, 8, tc, across);
-        write_rows<kFmt>(dup, a.along, a.rows, r0, second + c0, a.cols - c0, a.col_tiles + tc, across);
-    }
-    if (a.across.codes) {
-        write_cols<kFmt>(dgate, room, a.across, joined, col, kGroup, row, a.rows, tr);
-        write_cols<kFmt>(dup, room, a.across, joined, second + col, cols, row, a.rows, tr);
-    }
-    if (a.y.codes) write_cols<FP4Q_E4M3>(y, room, a.y, a.cols, col, cols, row, a.rows, tr);
 }
 
 template <typename T, int kAct>
