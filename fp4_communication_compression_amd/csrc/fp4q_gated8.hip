@@ -7,13 +7,13 @@
 // ends with both sums of an output in registers: the activation and the product are a few
 // operations on them, and neither g nor u need be written and read again.
 #include "fp4q_act.h"
-#include "fp4q_gemm8_plan.h"
+#include "fp4q_gated8_plan.h"
 #include "fp4q_gemm8_tile.h"
 
 namespace {
 
 using namespace fp4q_f8;
-using namespace fp4q_plan;
+using namespace fp4q_gated_plan;
 using namespace fp4q_tile;
 using namespace fp4q_act;
 
@@ -90,8 +90,6 @@ __global__ __launch_bounds__(kJoinThreads) void gated_join_kernel(GatedArgs p) {
 // branches around loads: what does not exist is read through an empty descriptor (behind a
 // branch the compiler would wait for all loads under way).  A load takes the whole 128 bytes
 // of 8 rows; they go through a part of LDS of the wavefront's own to the matrix core's rows.
-constexpr int kStripOut = 16;
-
 // `rows` rows of `pitch` bytes at `base`, the last one to be read up to `wide` bytes.
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_at(const uint8_t *base, int64_t first, int rows, int pitch, int wide) {
     const uint64_t at = (uint64_t)base + (uint64_t)(first * pitch);
@@ -254,6 +252,7 @@ __global__ __launch_bounds__(kWaves *kWave) void gated_strip_kernel(GatedArgs p)
 }
 
 using Large = Shape<2, 4, 8, 4>;   // 256 rows by 128 outputs, a workgroup a CU
+using Tall = Shape<2, 4, 6, 4>;    // 192 by 128, a workgroup a CU
 using Medium = Shape<2, 2, 4, 4>;  // 128 by 64, two workgroups a CU
 using Low64 = Shape<2, 2, 2, 4>;   // 64 by 64
 using Low32 = Shape<1, 4, 2, 2>;   // 32 by 64
@@ -286,25 +285,6 @@ bool bad_gated(int64_t M, int64_t N, int64_t K) {
     return M < 0 || N < 0 || K < 0 || M >= kLimit || N >= kLimit || K >= kLimit ||
            ceil_div(M, 32) * ceil_div(N, 64) > (int64_t)0x7FFFFFFF / 16;
 }
-// Strips for up to 16 rows of a, and for up to 64 where every unit has a workgroup and K is
-// short (us, weights from HBM; the tiles' time in brackets: 17 x 2752, K = 4096 9.8 (13.0), 48
-// x 2752, K = 4096 13.2 (16.0), 48 x 1024, K = 1024 5.9 (8.7); with more units a's rows are read
-// too often: 48 x 11008, K = 4096 31.7 (26.1); with long K too: 48 x 2752, K = 11008 28.7
-// (24.3)).  Else the product's plan of the joined rows: tiles of both halves' columns.
-Plan gated_plan(int64_t M, int64_t N, int64_t K) {
-    Plan plan = {Way::kStrip, kStrip, kStripOut, 1, 0, 0};
-    const bool few = M <= kStrip || (M <= 64 && N <= kStripOut * kCus && K <= 4096);
-    if (few && K > 0) return plan;
-    // (with K = 0 no strip, which would load a block that is not there; the tiles load none)
-    plan = plan_of(M <= kStrip ? kStrip + 1 : M, 2 * N, K, false);
-    plan.tile_n /= 2;
-    if (plan.parts > 1) {
-        plan.part_size = ceil_div(M * N, 4) * 4;
-        plan.workspace = (size_t)(2 * plan.part_size * plan.parts) * 4;
-    }
-    return plan;
-}
-
 }  // namespace
 
 extern "C" {
@@ -312,7 +292,7 @@ extern "C" {
 int fp4q_gated8_workspace(int64_t M, int64_t N, int64_t K, size_t *bytes) {
     if (bad_gated(M, N, K)) return FP4Q_ERR_SHAPE;
     if (!bytes) return FP4Q_ERR_NULL;
-    *bytes = M && N ? gated_plan(M, N, K).workspace : 0;
+    *bytes = M && N ? plan_of(M, N, K).workspace : 0;
     return FP4Q_OK;
 }
 
@@ -326,7 +306,7 @@ int fp4q_gated8(const uint8_t *a, int64_t a_pitch, int a_format, const float *a_
         bad_act(act))
         return FP4Q_ERR_ARG;
     if (M == 0 || N == 0) return FP4Q_OK;
-    const Plan plan = gated_plan(M, N, K);
+    const Plan plan = plan_of(M, N, K);
     if (!y || (K > 0 && (!a || !a_scales || !w || !w_scales)) || (plan.workspace && !workspace)) return FP4Q_ERR_NULL;
     if (!gate != !up) return FP4Q_ERR_NULL;
     if (!aligned(y, 16) || !aligned(gate, 16) || !aligned(up, 16) || !aligned(workspace, 16)) return FP4Q_ERR_ALIGN;
@@ -370,6 +350,7 @@ int fp4q_gated8(const uint8_t *a, int64_t a_pitch, int a_format, const float *a_
         case Way::kLow32: use(Low32{}); break;
         case Way::kLow64: use(Low64{}); break;
         case Way::kMedium: use(Medium{}); break;
+        case Way::kTall: use(Tall{}); break;
         case Way::kLarge: use(Large{}); break;
     }
     const int done = launch(fn, dim3((unsigned)(p.tiles_m * p.tiles_n * p.parts)), threads, args, stream);

@@ -4,7 +4,7 @@ import pytest
 torch = pytest.importorskip("torch")
 
 from tests import gated_ref as gref
-from tests import gemm_shapes
+from tests import gated_shapes
 from tests import linear_ref as ref
 from tests.linear_ref import HALF_STEP, U
 from tests.test_linear_gpu import down, fp4q, same, up, within  # noqa: F401 (fp4q is the fixture)
@@ -89,22 +89,13 @@ def test_gated(fp4q, shape, act):
     assert torch.equal(alone.y, got.y)
 
 
-# rows, columns and length; the rows of the kernel's tile, its columns, runs of K
-KERNELS = [(16, 2048, 1111, 16, 8, 1), (3, 133, 2222, 16, 8, 1),
-           (600, 260, 900, 32, 64, 1), (48, 257, 2222, 32, 64, 6),
-           (5000, 260, 1111, 64, 64, 1), (2049, 750, 640, 64, 64, 1), (3000, 129, 2222, 64, 64, 3),
-           (1030, 3000, 1111, 128, 64, 1), (4099, 752, 1024, 128, 64, 1), (6000, 129, 4001, 128, 64, 3),
-           (2049, 3000, 1111, 256, 128, 1), (3000, 2052, 1024, 256, 128, 1), (130, 4100, 16000, 256, 128, 7)]
-
-
-@pytest.mark.parametrize("shape", KERNELS)
+@pytest.mark.parametrize("shape", gated_shapes.SHAPES)
 @pytest.mark.parametrize("fa", [E4M3, E5M2])
 @pytest.mark.parametrize("fw", [E4M3, E5M2])
 def test_every_kernel(fp4q, shape, fa, fw):
     print(shape, fa, fw, flush=True)
     m, n, k = shape[:3]
-    rows, cols, runs = gemm_shapes.plan(m, 2 * n, k, False)
-    assert (rows, cols // 2, runs) == shape[3:]
+    assert gated_shapes.plan(m, n, k) == shape[3:]
     ops = operands(m, n, k, fa, fw)
     got = fp4q.fp4q_gated8(*ops, "silu", want_pre=True)
     check_gated(got, halves(*ops), "silu", True)
