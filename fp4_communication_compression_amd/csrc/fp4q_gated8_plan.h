@@ -26,10 +26,13 @@ struct Plan {
 // (24.3)).
 // Else the least of an estimate as for fp4q_gemm8: a tile's block of K costs block_us with one,
 // two or three workgroups on a CU and its beginning and end, the activation and three outputs
-// among them, cost start_us; fitted to the tiles' times with every CU full at K = 2048 and 8192.
-// It gives 2047 x 2752, K = 4096 within 4 % of the 57.8 us that 192-row tiles take there (256
-// rows: 67.4, 128 x 64: 71.4, 64 x 64: 81.0), and 8192 x 11008 the 256-row tiles (756; 192 rows
-// 827, 128 x 64 900, 64 x 64 1097).  Runs of K are added by a second launch.
+// among them, cost start_us; fitted to the times of every tile with 1 to 6 runs over 13 products
+// (48 x 11008 to 8192 x 11008, K = 4096 and 11008) and to the tiles' alone with every CU full.
+// Over those products the choice takes 3 % longer than the best way on average, 11 % at most
+// (128 x 2752, K = 11008).  At K = 4096: 2047 x 2752 57.8 us in 192-row tiles (256 rows 67.4, 128
+// x 64 71.4, 64 x 64 81.0), 8192 x 11008 756 in 256-row tiles (827, 900, 1097), 48 x 11008 26.5 in
+// 64 x 64 tiles and two or four runs (32 x 64 29.2, whole 32.3).  Runs of K are added by a second
+// launch.
 inline Plan plan_of(int64_t M, int64_t N, int64_t K) {
     Plan plan = {Way::kStrip, 64, kStripOut, 1, 0, 0};
     const bool few = M <= 16 || (M <= 64 && N <= (int64_t)kStripOut * kCus && K <= 4096);
@@ -39,12 +42,12 @@ inline Plan plan_of(int64_t M, int64_t N, int64_t K) {
         int m, n, per_cu;
         double start_us, block_us[3];
     };
-    static const Kind kinds[] = {{Way::kLow32, 32, 64, 3, 1.0, {0.55, 0.60, 0.72}},
-                                 {Way::kLow64, 64, 64, 3, 2.5, {0.60, 0.66, 1.03}},
-                                 {Way::kMedium, 128, 64, 2, 4.5, {0.72, 0.99}},
-                                 {Way::kTall, 192, 128, 1, 5.0, {1.53}},
-                                 {Way::kLarge, 256, 128, 1, 8.4, {1.91}}};
-    constexpr double kLaunchUs = 4.7, kJoinUs = 1.5, kJoinUsPerPart = 0.25, kJoinUsPerSum = 1.1e-6;
+    static const Kind kinds[] = {{Way::kLow32, 32, 64, 3, 1.3, {0.62, 0.75, 0.96}},
+                                 {Way::kLow64, 64, 64, 3, 2.9, {0.69, 0.77, 1.18}},
+                                 {Way::kMedium, 128, 64, 2, 3.1, {0.79, 1.04}},
+                                 {Way::kTall, 192, 128, 1, 4.0, {1.47}},
+                                 {Way::kLarge, 256, 128, 1, 6.8, {1.80}}};
+    constexpr double kLaunchUs = 4.7, kJoinUs = 1.5, kJoinUsPerPart = 0.4, kJoinUsPerSum = 1.03e-6;
     const int64_t blocks = ceil_div(K, kGroup);
     double best = 1e300;
     for (const Kind &k : kinds) {
