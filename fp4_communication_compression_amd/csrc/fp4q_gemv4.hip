@@ -51,6 +51,32 @@ struct Gemv4Args {
 // 128, so quarter q needs columns 128 h + 32 q + 8 j; they lie at 16 h + 4 j + q.
 __device__ __forceinline__ int place_of(int k) { return (k & 128) | (k & 24) << 2 | (k & 96) >> 2 | (k & 7); }
 
+// The value of another lane of the same 16 (a DPP control), and a swap of a's odd rows of 16
+// lanes with b's even ones (or of a's upper 32 lanes with b's lower ones).
+template <int kControl>
+__device__ __forceinline__ float moved(float v) {
+    return __uint_as_float((unsigned)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(v), kControl, 0xF, 0xF, true));
+}
+__device__ __forceinline__ void exchange(int far, float &a, float &b) {
+    const unsigned x = __float_as_uint(a), y = __float_as_uint(b);
+    if (far == 16) {
+        const auto r = __builtin_amdgcn_permlane16_swap(x, y, false, false);
+        a = __uint_as_float(r[0]);
+        b = __uint_as_float(r[1]);
+    } else {
+        const auto r = __builtin_amdgcn_permlane32_swap(x, y, false, false);
+        a = __uint_as_float(r[0]);
+        b = __uint_as_float(r[1]);
+    }
+}
+__device__ __forceinline__ unsigned most64(unsigned v) {
+    v = max16(v);
+    const auto r = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+    v = umax(r[0], r[1]);
+    const auto q = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    return umax(q[0], q[1]);
+}
+
 // A block of 256 of a row, four neighbours a lane of a wavefront.
 struct Rowblock {
     float v[4];
@@ -64,7 +90,8 @@ struct Rowblock {
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[i] = __uint_as_float(i & 1 ? w[i >> 1] & 0xFFFF0000u : w[i >> 1] << 16);
     }
-    // y = H v / 16 in fp32: strides 1 and 2 in a lane, 4 to 128 over the lanes.
+    // y = H v / 16 in fp32: strides 1 and 2 in a lane, 4 to 128 over the lanes, by exchanges
+    // within rows of 16 lanes and between the rows.
     __device__ __forceinline__ void transform() {
         const int lane = threadIdx.x & (kWave - 1);
         const float a = v[0] + v[1], b = v[0] - v[1], c = v[2] + v[3], d = v[2] - v[3];
@@ -72,15 +99,25 @@ struct Rowblock {
         v[1] = b + d;
         v[2] = a - c;
         v[3] = b - d;
+        auto within = [&](int far, auto partner) {
+            const float sign = lane & far ? -1.0f : 1.0f;
 #pragma unroll
-        for (int far = 1; far < kWave; far *= 2) {
-            const bool second = lane & far;
+            for (int i = 0; i < 4; ++i) v[i] = fmaf(v[i], sign, partner(v[i]));  // (exact: a sum or a difference)
+        };
+        within(1, [](float x) { return moved<0xB1>(x); });                 // lanes 1 0 3 2
+        within(2, [](float x) { return moved<0x4E>(x); });                 // lanes 2 3 0 1
+        within(4, [](float x) { return moved<0x141>(moved<0x1B>(x)); });   // lanes 3 2 1 0 of four, then 7 .. 0 of eight
+        within(8, [](float x) { return moved<0x128>(x); });                // a turn by 8 of 16
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float other = __shfl_xor(v[i], far);
-                v[i] = second ? other - v[i] : v[i] + other;
+        for (int far = 16; far <= 32; far *= 2)
+#pragma unroll
+            for (int i = 0; i < 4; i += 2) {
+                exchange(far, v[i], v[i + 1]);  // one register gets both first halves, the other both second ones
+                const float sum = v[i] + v[i + 1], difference = v[i] - v[i + 1];
+                v[i] = sum;
+                v[i + 1] = difference;
+                exchange(far, v[i], v[i + 1]);
             }
-        }
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[i] *= 0.0625f;
     }
@@ -93,7 +130,7 @@ struct Rowblock {
         unsigned top = 0;
 #pragma unroll
         for (int i = 0; i < 4; ++i) top = umax(top, mag(v[i]));
-        top = max64(top);
+        top = most64(top);
         const bool finite = top < 0x7F800000u;
         const int e = finite ? max((int)(top >> 23) - 127, -84) : 14;
         const float power = __uint_as_float((unsigned)(127 + 14 - e) << 23);
@@ -299,12 +336,11 @@ __global__ __launch_bounds__(kWaves *kWave) void gemv4_kernel(Gemv4Args p) {
         });
     };
     if constexpr (kStage) {
-        // the loads of x first: a wavefront's loads return in order
-        int at = wave;
-        Rowblock r;
-        r = ready(p, m0 + min(at, rows * blocks - 1) / blocks, min(at, rows * blocks - 1) % blocks);
+        // the first loads of x before the weight's: a wavefront's loads return in order
+        const int all = rows * blocks;
+        Rowblock r = ready(p, m0 + min(wave, all - 1) / blocks, min(wave, all - 1) % blocks);
         load_first();
-        for (; at < rows * blocks; at += kWaves) {
+        for (int at = wave; at < all; at += kWaves) {
             const int row = at / blocks, kb = at % blocks;
             if (at != wave) r = ready(p, m0 + row, kb);
             if (p.transform) r.transform();
@@ -405,20 +441,25 @@ int check_sizes(int64_t M, int64_t K, int dtype, uint32_t flags) {
     if (flags & ~(uint32_t)FP4Q_FLAG_NO_FWHT) return FP4Q_ERR_ARG;
     return dtype == FP4Q_OUT_F32 || dtype == FP4Q_OUT_BF16 ? FP4Q_OK : FP4Q_ERR_ARG;
 }
-int parts_of(int dtype, uint32_t flags) { return dtype == FP4Q_OUT_F32 || !(flags & FP4Q_FLAG_NO_FWHT) ? 2 : 1; }
-
-// Whether every workgroup makes x ready itself, which saves a launch: for as many blocks of
-// 256 of x as its wavefronts do while the weight's first loads are on their way (one row of
-// 11008: 10.3 us instead of 13.5; 4 rows of 4096: 18.0 instead of 20.5 with two payloads of
-// 11008 rows; 5 transformed rows of 4096, 80 blocks: 27.7 instead of 11.9).
-constexpr int kStageBlocks = 64, kStageLds = 64 * 1024;
-int64_t staged_bytes(int64_t cols, int64_t K) { return cols * (2 * (K + 8) + 4 * (K / kBlock)); }
-bool staged(int64_t M, int64_t K, int parts) {
-    return M * parts <= 16 && M * (K / kBlock) <= kStageBlocks && staged_bytes(M * parts, K) <= kStageLds;
+// Transformed bf16 x takes one part where out is bf16: 11 bits of values that come from 8.
+int parts_of(int dtype, int out_dtype, uint32_t flags) {
+    return dtype == FP4Q_OUT_F32 || (!(flags & FP4Q_FLAG_NO_FWHT) && out_dtype == FP4Q_OUT_F32) ? 2 : 1;
 }
-size_t workspace_of(int64_t M, int64_t K, int dtype, uint32_t flags) {
-    const int parts = parts_of(dtype, flags);
-    return staged(M, K, parts) ? 0 : (size_t)(M * parts * (2 * K + 4 * (K / kBlock)));
+
+// Whether every workgroup makes x ready itself, which saves a launch, for as many blocks of 256
+// of x as its wavefronts do while the weight's first loads are on their way (one that has to be
+// transformed counts twice).  us, payloads from HBM, the other way in brackets: one row of 11008
+// 10.1 (13.3), two 11.7 (13.9); 8 rows of 4096 with two payloads of 11008 rows 20.0 (20.8), with
+// one of 4096 rows 10.5 (10.0); 4 transformed rows of 4096 10.6 (10.5), 5 12.9 (11.7).
+constexpr int kStageBlocks = 128, kLds = 160 * 1024;
+int64_t staged_bytes(int64_t cols, int64_t K) { return cols * (2 * (K + 8) + 4 * (K / kBlock)); }
+bool staged(int64_t M, int64_t K, int parts, uint32_t flags) {
+    const int64_t cols = M * parts, rest = 16 * (2 * 2 * cols * 64 + (int64_t)sizeof(Turn));  // of the widest kernel
+    const int64_t work = M * (K / kBlock) * (flags & FP4Q_FLAG_NO_FWHT ? 1 : 2);
+    return cols <= 16 && work <= kStageBlocks && staged_bytes(cols, K) + rest <= kLds;
+}
+size_t workspace_of(int64_t M, int64_t K, int parts, uint32_t flags) {
+    return staged(M, K, parts, flags) ? 0 : (size_t)(M * parts * (2 * K + 4 * (K / kBlock)));
 }
 
 template <int kWaves, int kCols, int kStrips, int kBlocksAhead, bool kGated, Source kSource>
@@ -450,7 +491,7 @@ int run_product(Gemv4Args &p, bool stage, void *stream) {
     constexpr int kS = kGated ? 2 : 1;
     const int64_t cols = (int64_t)p.M * p.parts, blocks = p.K / kBlock;
     if (stage) {
-        if (!kGated && blocks > 16) return run_kernel<16, 1, kS, 1, kGated, Source::kStaged>(p, kCus, stream);
+        if ((!kGated && blocks > 16) || p.M * blocks > 32) return run_kernel<16, 1, kS, 1, kGated, Source::kStaged>(p, kCus, stream);
         return run_kernel<8, 1, kS, 1, kGated, Source::kStaged>(p, 2 * kCus, stream);
     }
     if (cols <= 16 && blocks <= 16) return run_kernel<16, 1, kS, 3 - kS, kGated, Source::kOne>(p, kCus, stream);
@@ -465,7 +506,8 @@ int run(const void *x, int dtype, int64_t M, const Payload &w, const Payload *up
     if (st != FP4Q_OK) return st;
     if ((out_dtype != FP4Q_OUT_F32 && out_dtype != FP4Q_OUT_BF16) || bad_act(act)) return FP4Q_ERR_ARG;
     if (M == 0 || N == 0) return FP4Q_OK;
-    const size_t need = workspace_of(M, K, dtype, flags);
+    const int parts = parts_of(dtype, out_dtype, flags);
+    const size_t need = workspace_of(M, K, parts, flags);
     const Payload weights[] = {w, up ? *up : w};
     if (!x || !out || (need && !workspace)) return FP4Q_ERR_NULL;
     for (const Payload &q : weights)
@@ -482,7 +524,6 @@ int run(const void *x, int dtype, int64_t M, const Payload &w, const Payload *up
         ins[3 + 3 * i] = rng(weights[i].block, 4 * N * (K / kBlock));
     }
     if (clash(outs, 2, ins, 7)) return FP4Q_ERR_ARG;
-    const int parts = parts_of(dtype, flags);
     Gemv4Args p = {x, nullptr, weights[0], weights[1], out, (int)M, (int)N, (int)K, parts, act,
                    out_dtype == FP4Q_OUT_F32, dtype == FP4Q_OUT_F32, !(flags & FP4Q_FLAG_NO_FWHT)};
     if (need) {
@@ -506,7 +547,9 @@ int fp4q_gemv4_workspace(int64_t M, int64_t K, int dtype, uint32_t flags, size_t
     const int st = check_sizes(M, K, dtype, flags);
     if (st != FP4Q_OK) return st;
     if (!bytes) return FP4Q_ERR_NULL;
-    *bytes = workspace_of(M, K, dtype, flags);
+    // enough for either type of out
+    *bytes = std::max(workspace_of(M, K, parts_of(dtype, FP4Q_OUT_F32, flags), flags),
+                      workspace_of(M, K, parts_of(dtype, FP4Q_OUT_BF16, flags), flags));
     return FP4Q_OK;
 }
 

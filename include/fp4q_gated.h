@@ -91,7 +91,8 @@ int fp4q_gated8_backward(const void *dy, const void *gate, const void *up, int64
  * The codes times their micro-scales are exact in fp16.  x becomes fp16 under a power of two
  * (2^98 at most) for each row and block of 256: bf16 x exactly, but for values 2^-28 below
  * the block's largest; fp32 or transformed x in two parts, to 2^-22 of each value (and
- * 2^-39 of the block's largest).  Products are exact and added in fp32 by the matrix core, a
+ * 2^-39 of the block's largest), but for transformed bf16 x with bf16 out, which takes one
+ * part, to 2^-11 (x itself has 8 bits, and so has out).  Products are exact and added in fp32 by the matrix core, a
  * block's sum times its scale in fp32.  As for fp4q_compress, x must be finite with
  * |x| < 2^118, which is not checked (a row of x that is not gives a row of out that is not);
  * of x what lies below 2^-112, and of a block's sum what lies below 2^-126 before its scale

@@ -69,15 +69,15 @@ def payload_values(payload):
     return v * block.double().repeat_interleave(256, 1)
 
 
-def gemv4(x, payload, transformed):
+def gemv4(x, payload, transformed, parts=2):
     """x times the payload's weight, transposed, in 64 bits, and the bound of the kernel's fp32
     sum: 256 additions of a block and three parts (a whole step each, whatever way the matrix
     core rounds), the block's scale, an addition a block and the join of 16 wavefronts.  A
     transformed weight is H Q / 16: x is transformed in fp32 instead, eight stages of one
     rounding each on sums of at most the block's |x|, and a multiplication by 1/16 (exact).
     As fp16 under its block's power of two, the largest at 2^14 or more: a part that is a
-    normal number is within 2^-11 of its value, two parts within 2^-22; a part below 2^-14
-    may count as zero, 2^-28 of the largest."""
+    normal number is within 2^-11 of its value, two parts within 2^-22 (one part only where
+    transformed bf16 x has bf16 out); a part below 2^-14 may count as zero, 2^-28 of the largest."""
     q, x = payload_values(payload), x.double().cpu()
     m, k = x.shape
     off_x = torch.zeros_like(x)
@@ -86,6 +86,6 @@ def gemv4(x, payload, transformed):
         off_x = 8 * U * spread
         x = (x.view(m, -1, 256) @ hadamard()).reshape(m, k) / 16
     top = x.abs().view(m, -1, 256).amax(dim=2).repeat_interleave(256, 1)
-    off_x = off_x + 4 * U * x.abs() + 2.0 ** -28 * top
+    off_x = off_x + (4 * U if parts == 2 else 2.0 ** -11) * x.abs() + 2.0 ** -28 * top
     want = x @ q.t()
     return want, (x.abs() @ q.abs().t()) * U * (2 * 256 + k // 256 + 16 + 8) + off_x @ q.abs().t()
