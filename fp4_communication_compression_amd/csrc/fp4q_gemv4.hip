@@ -434,10 +434,11 @@ __global__ __launch_bounds__(kWaves *kWave) void gemv4_kernel(Gemv4Args p) {
 }
 
 // ------------------------------------------------------------------------ host
-constexpr int64_t kLimit = kDimLimit / 2, kLimitK = (int64_t)1 << 24;
+// M: so that the chunks of 16 rows or more are a grid's second dimension
+constexpr int64_t kLimit = kDimLimit / 2, kLimitM = (int64_t)1 << 19, kLimitK = (int64_t)1 << 24;
 
 int check_sizes(int64_t M, int64_t K, int dtype, uint32_t flags) {
-    if (M < 0 || K <= 0 || M >= kLimit || K >= kLimitK || K % kBlock) return FP4Q_ERR_SHAPE;
+    if (M < 0 || K <= 0 || M >= kLimitM || K >= kLimitK || K % kBlock) return FP4Q_ERR_SHAPE;
     if (flags & ~(uint32_t)FP4Q_FLAG_NO_FWHT) return FP4Q_ERR_ARG;
     return dtype == FP4Q_OUT_F32 || dtype == FP4Q_OUT_BF16 ? FP4Q_OK : FP4Q_ERR_ARG;
 }
@@ -468,7 +469,7 @@ int run_kernel(Gemv4Args &p, int most, void *stream) {
     void *args[] = {&p};
     const int64_t units = ceil_div(p.N, kGated ? kStrip : kStrip * kStrips), chunks = ceil_div(p.M, each);
     const dim3 grid((unsigned)std::min<int64_t>(units, most), (unsigned)chunks);
-    if (chunks > 65535) return FP4Q_ERR_SHAPE;
+    static_assert(kLimitM / 16 <= 65535, "chunks");
     const int64_t cols = std::min<int64_t>(each, p.M) * p.parts;
     const int64_t lds = kWaves * (2 * kStrips * cols * 64 + (int64_t)sizeof(Turn)) +
                         (kSource == Source::kStaged ? staged_bytes(p.M * p.parts, p.K) : 0);
@@ -478,11 +479,12 @@ int run_kernel(Gemv4Args &p, int most, void *stream) {
 }
 // The kernel and the number of its workgroups, one or two a CU.  Measured (us, payloads from
 // HBM; the other way in brackets):
-//   16 wavefronts for one row of long K: 4096 x 11008 10.3 (8 of them: 12.3); 8 for K <= 4096,
-//   which two workgroups a CU then share: 1024 x 1024 3.7 (4.6), 11008 x 4096 gated 13.7 (15.5)
+//   x made ready in the kernel: 16 wavefronts for one row of long K, 4096 x 11008 10.1 (8 of them:
+//   12.3), and for more than 32 blocks of x; else 8, two workgroups a CU: 1024 x 1024 3.7 (4.6),
+//   11008 x 4096 gated 13.7 (15.5)
 //   x in registers where 16 wavefronts have a block each: 16 x 32768 x 4096 22.5 (24.9 without
-//   the second block's loads ahead; gated, whose two strips leave no registers for those, 22.2
-//   against 34)
+//   the second block's loads ahead); gated, where two strips leave no registers for those, with
+//   more than one unit a workgroup: 16 x 11008 x 4096 22.6 (27.5), but 16 x 2752 14.3 (13.5)
 //   two strips, which share x, for two column tiles: 64 x 4096 x 4096 19.0 (30.8 with one); one
 //   strip, and more workgroups, for one: 16 x 4096 x 11008 21.8 (24.1)
 constexpr int kCus = 256;
@@ -494,7 +496,8 @@ int run_product(Gemv4Args &p, bool stage, void *stream) {
         if ((!kGated && blocks > 16) || p.M * blocks > 32) return run_kernel<16, 1, kS, 1, kGated, Source::kStaged>(p, kCus, stream);
         return run_kernel<8, 1, kS, 1, kGated, Source::kStaged>(p, 2 * kCus, stream);
     }
-    if (cols <= 16 && blocks <= 16) return run_kernel<16, 1, kS, 3 - kS, kGated, Source::kOne>(p, kCus, stream);
+    if (cols <= 16 && blocks <= 16 && (!kGated || p.N > kStrip * kCus))
+        return run_kernel<16, 1, kS, 3 - kS, kGated, Source::kOne>(p, kCus, stream);
     if (cols <= 16) return run_kernel<8, 1, kS, 1, kGated, Source::kMemory>(p, kCus, stream);
     return run_kernel<8, 2, 2, 1, kGated, Source::kMemory>(p, kCus, stream);
 }

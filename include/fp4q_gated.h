@@ -15,7 +15,8 @@
  * flags, formats, types and activation, then NULL, alignment, workspace size (FP4Q_ERR_SHAPE)
  * and overlap of an output with an input or another output (FP4Q_ERR_ARG)), FP4Q_ERR_LAUNCH
  * for a failed launch.  Tensors, codes, micro-scales and workspaces are aligned to 16 bytes,
- * scales to 4.  Results do not depend on timing: no atomics, every sum in a fixed order.
+ * scales to 4.  A size that would need more than 2^32 - 1 threads returns FP4Q_ERR_SHAPE.
+ * Results do not depend on timing: no atomics, every sum in a fixed order.
  *
  * Joined halves.  The weights of the gate and the up projection, N rows each, are one operand
  * of R = P + N rows, where P = N rounded up to a multiple of 128: the gate's rows, rows of
@@ -72,7 +73,8 @@ int fp4q_gated8(const uint8_t *a, int64_t a_pitch, int a_format, const float *a_
  *                        y_t_pitch, and scales [ceil(rows/128) x cols]: the operand of the
  *                        second projection's weight gradient
  * Each is what fp4q_quantize8 makes of the fp32 tensor.  Each pair may be NULL, not all
- * three.  rows >= 0, 1 <= cols; rows, cols < 2^27, fewer than 2^31 tiles of 128 x 128. */
+ * three.  gate and up must be finite where their results count.  rows >= 0, 1 <= cols;
+ * rows, cols < 2^27. */
 int fp4q_gated8_backward(const void *dy, const void *gate, const void *up, int64_t rows, int64_t cols,
                          int dtype, int act, int format, uint8_t *codes, int64_t code_pitch,
                          float *scales, uint8_t *codes_t, int64_t code_t_pitch, float *scales_t,
@@ -97,7 +99,7 @@ int fp4q_gated8_backward(const void *dy, const void *gate, const void *up, int64
  * |x| < 2^118, which is not checked (a row of x that is not gives a row of out that is not);
  * of x what lies below 2^-112, and of a block's sum what lies below 2^-126 before its scale
  * (times 2^17), may be dropped.
- * 0 <= M, N < 2^27, 0 < K < 2^24. */
+ * 0 <= M < 2^19, 0 <= N < 2^27, 0 < K < 2^24. */
 int fp4q_gemv4_workspace(int64_t M, int64_t K, int dtype, uint32_t flags, size_t *bytes);
 int fp4q_gemv4(const void *x, int dtype, int64_t M, const uint8_t *codes, const uint8_t *micro_scales,
                const float *block_scales, int64_t N, int64_t K, void *out, int out_dtype,

@@ -9,7 +9,7 @@ import os
 HERE = os.path.dirname(os.path.abspath(__file__))
 
 SHAPES = [(16, 2048, 1111, 64, 16, 1), (3, 133, 2222, 64, 16, 1), (24, 260, 900, 64, 16, 1), (64, 333, 2222, 64, 16, 1),
-          (40, 4096, 1000, 64, 16, 1),
+          (32, 4096, 1111, 64, 16, 1), (40, 4096, 1000, 64, 16, 1),
           (600, 260, 900, 32, 64, 1), (4296, 40, 1277, 32, 64, 1), (100, 257, 2222, 32, 64, 6), (48, 264, 4222, 32, 64, 7),
           (5000, 260, 1111, 64, 64, 1), (2049, 752, 640, 64, 64, 1), (37, 8486, 2266, 64, 64, 3),
           (1030, 3000, 1111, 128, 64, 1), (4099, 750, 1024, 128, 64, 1), (6000, 129, 4001, 128, 64, 3),

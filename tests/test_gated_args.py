@@ -278,7 +278,7 @@ def gated4(x=G, dtype=1, m=3, codes=2 * G, micro=3 * G, block=4 * G, n=6, k=512,
 
 
 BOTH = [({"m": -1}, SHAPE), ({"n": -1}, SHAPE), ({"k": 0}, SHAPE), ({"k": 300}, SHAPE), ({"k": 1 << 24}, SHAPE),
-        ({"m": 1 << 27}, SHAPE), ({"n": 1 << 27}, SHAPE), ({"flags": 2}, ARG), ({"dtype": 2}, ARG), ({"out_dtype": -1}, ARG),
+        ({"m": 1 << 19}, SHAPE), ({"n": 1 << 27}, SHAPE), ({"flags": 2}, ARG), ({"dtype": 2}, ARG), ({"out_dtype": -1}, ARG),
         ({"m": 0, "x": None}, OK), ({"n": 0, "codes": None}, OK), ({"x": None}, NULL), ({"codes": None}, NULL),
         ({"micro": None}, NULL), ({"block": None}, NULL), ({"out": None}, NULL), ({"m": 100, "space": None}, NULL),
         ({"m": 100, "size": 1000}, SHAPE), ({"x": G + 8}, ALIGN), ({"codes": 2 * G + 8}, ALIGN), ({"micro": 3 * G + 4}, ALIGN),

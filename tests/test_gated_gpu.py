@@ -520,6 +520,26 @@ def test_training_on_streams_and_in_graphs(fp4q, tokens):
         assert all(torch.equal(a, b) for a, b in zip(run(), held)), turn
 
 
+@pytest.mark.parametrize("ranks,tokens,hidden,inner", [(2, 96, 512, 1024), (4, 7, 256, 528), (1, 200, 512, 300)])
+def test_example_layer_gated(fp4q, ranks, tokens, hidden, inner):
+    """The gated layer of examples/tp_layer.py against fp32: the bounds of the two products above,
+    and FP4's 0.15 in the norm at each of two exchanges."""
+    from examples import tp_layer
+    plain = tp_layer.errors(ranks, tokens, hidden, inner, compress=False, gated=True)
+    fp4 = tp_layer.errors(ranks, tokens, hidden, inner, compress=True, gated=True)
+    print(plain, fp4, flush=True)
+    assert max(plain.values()) < 0.2
+    assert max(fp4.values()) < 0.5
+
+
+def test_example_token(fp4q):
+    """A 4-bit weight is off by at most 0.25 of a value, 0.15 in the norm, of a product as much;
+    the activation's product doubles it and the second projection adds its own."""
+    from examples import tp_layer
+    assert tp_layer.token_error(2, 3, 512, 1024) < 0.5
+    assert tp_layer.token_error(2, 1, 512, 600) < 0.5    # a shard of 300: padded
+
+
 def serving(fp4q, x, w, gate, u, down_w, flags, stream=None):
     """One step of single tokens through the same layer with 4-bit weights."""
     n = fp4q.fp4q_rmsnorm(x, w, 1e-6, stream=stream).y
