@@ -35,19 +35,19 @@ __device__ __forceinline__ float largest(float a, float b, float c) {
     return __builtin_elementwise_maximum(__builtin_elementwise_maximum(fabsf(a), fabsf(b)), fabsf(c));
 }
 
-// Codes along the rows of a tile: row r0 + i of `rows`, group `group` of `out`, columns
-// c0 .. c0 + 7 of the tensor of which `left` exist.
+// Codes of eight neighbours of a tile's row, `left` of which exist, to offset `at` of the tile's
+// codes, and the row's scale to its place among the tile's.
 template <int kFmt>
-__device__ __forceinline__ void write_row(const float (&v)[8], const Codes &out, int rows, int row, int c0, int left,
-                                          int group, int across) {
+__device__ __forceinline__ void write_row(const float (&v)[8], uint8_t *codes, float *scales, bool exists, unsigned at,
+                                          int row, int left, int across) {
     const float top = largest(largest(largest(v[0], v[1], v[2]), v[3], v[4]), v[5], largest(v[6], v[7], v[7]));
     const Scale sc = scale_of<kFmt>(max16(mag(top)));
     u32x2 w;
     w[0] = code_quad<kFmt>(v[0], v[1], v[2], v[3], sc);
     w[1] = code_quad<kFmt>(v[4], v[5], v[6], v[7], sc);
-    if (row >= rows) return;
-    if (across == 0) out.scales[(int64_t)group * rows + row] = sc.s;
-    store_bytes8(out.codes + (int64_t)row * out.pitch + c0, left, w);
+    if (!exists) return;
+    if (across == 0) scales[row] = sc.s;
+    store_bytes8(codes + at, left, w);
 }
 
 // Thread t holds rows kRows (t / 16) + i and columns 8 (t % 16) + j of the tile.
@@ -61,7 +61,11 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2) void gated_grad_k
     const int t = threadIdx.x, lane = t & (kWave - 1), wave = t / kWave, across = t & 15, down = t >> 4;
     const int tc = (int)(blockIdx.x % (unsigned)a.col_tiles), tr = (int)(blockIdx.x / (unsigned)a.col_tiles);
     const int row = tr * kGroup, col = tc * kGroup, r0 = row + kRows * down, c0 = col + 8 * across;
-    const int64_t from = (int64_t)r0 * a.cols + c0;
+    // places in memory: of the tile, the same for all lanes, in 64 bits; within it in 32
+    const int64_t tile = (int64_t)row * a.cols + col;
+    auto of_tile = [&](const void *base, unsigned bytes) {
+        return reinterpret_cast<const T *>(reinterpret_cast<const char *>(static_cast<const T *>(base) + tile) + bytes);
+    };
     // the joined tensor: columns N .. P of its first half are zeros, as those of the tile are
     const int second = a.col_tiles * kGroup;
     const int64_t joined = (int64_t)second + a.cols;
@@ -71,11 +75,14 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2) void gated_grad_k
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
         const int left = r0 + i < a.rows ? a.cols - c0 : 0;
-        const int64_t at = from + (int64_t)i * a.cols;
-        dy[i].template load<kWhole>(static_cast<const T *>(a.dy) + at, left);
-        gate[i].template load<kWhole>(static_cast<const T *>(a.gate) + at, left);
-        up[i].template load<kWhole>(static_cast<const T *>(a.up) + at, left);
+        const unsigned at = ((unsigned)(kRows * down + i) * (unsigned)a.cols + 8 * across) * (unsigned)sizeof(T);
+        dy[i].template load<kWhole>(of_tile(a.dy, at), left);
+        gate[i].template load<kWhole>(of_tile(a.gate, at), left);
+        up[i].template load<kWhole>(of_tile(a.up, at), left);
     }
+    const int64_t along = row * a.along.pitch + col;
+    float *const gate_scales = a.along.scales + (int64_t)tc * a.rows + row;
+    float *const up_scales = gate_scales + (int64_t)a.col_tiles * a.rows;
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
         float d[8], g[8], u[8];
@@ -90,8 +97,10 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2) void gated_grad_k
             v[kY][i][j] = f.act * u[j];
         }
         if (a.along.codes) {
-            write_row<kFmt>(v[kGate][i], a.along, a.rows, r0 + i, c0, 8, tc, across);
-            write_row<kFmt>(v[kUp][i], a.along, a.rows, r0 + i, second + c0, a.cols - c0, a.col_tiles + tc, across);
+            const int r = kRows * down + i;
+            const unsigned at = (unsigned)r * (unsigned)a.along.pitch + 8 * across;
+            write_row<kFmt>(v[kGate][i], a.along.codes + along, gate_scales, r0 + i < a.rows, at, r, 8, across);
+            write_row<kFmt>(v[kUp][i], a.along.codes + along + second, up_scales, r0 + i < a.rows, at, r, a.cols - c0, across);
         }
     }
     if (!a.across.codes && !a.y.codes) return;
@@ -147,13 +156,14 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2) void gated_grad_k
     for (int k = 0; k < kTensors; ++k) {
         const Codes &out = k == kY ? a.y : a.across;
         if (!out.codes) continue;
+        uint8_t *const codes = out.codes + ((k == kUp ? second : 0) + col) * out.pitch + row;
 #pragma unroll
         for (int n = 0; n < kGroup / (kThreads / 8); ++n) {
             const int c = n * (kThreads / 8) + t / 8, key = c / 8;
             const u32x4 q = reinterpret_cast<const u32x4 *>(room.turn[k])[c * 8 + (pair ^ (key >> 1))];
             const u32x4 w = key & 1 ? u32x4{q[2], q[3], q[0], q[1]} : q;
             if ((k == kGate || c < cols) && at < a.rows) {
-                uint8_t *p = out.codes + (int64_t)((k == kUp ? second : 0) + col + c) * out.pitch + at;
+                uint8_t *p = codes + ((unsigned)c * (unsigned)out.pitch + 16 * pair);
                 if (a.rows - at >= 16) {
                     __builtin_nontemporal_store(w, reinterpret_cast<u32x4 *>(p));
                 } else {
@@ -174,19 +184,24 @@ const void *pick(int fmt, bool whole) {
                  : (const void *)&gated_grad_kernel<T, kAct, FP4Q_E5M2, false>;
 }
 
+// So that a tile's places in any of the arrays are offsets of 32 bits.
+constexpr int64_t kLimit = (int64_t)1 << 23;
+static_assert((kGroup - 1) * kLimit * 4 + kGroup * 4 < ((int64_t)1 << 32), "of 128 rows of floats");
+static_assert((kGroup - 1) * 4 * kLimit + kGroup < ((int64_t)1 << 32), "of 128 pitches");
+
 }  // namespace
 
 extern "C" int fp4q_gated8_backward(const void *dy, const void *gate, const void *up, int64_t rows, int64_t cols,
                                     int dtype, int act, int format, uint8_t *codes, int64_t code_pitch,
                                     float *scales, uint8_t *codes_t, int64_t code_t_pitch, float *scales_t,
                                     uint8_t *y_codes_t, int64_t y_t_pitch, float *y_scales_t, void *stream) {
-    if (bad_dims(rows, cols) || rows >= kDimLimit / 2 || cols >= kDimLimit / 2) return FP4Q_ERR_SHAPE;
+    if (bad_dims(rows, cols) || rows >= kLimit || cols >= kLimit) return FP4Q_ERR_SHAPE;
     const int64_t row_tiles = ceil_div(rows, kGroup), col_tiles = ceil_div(cols, kGroup);
     const int64_t joined = col_tiles * kGroup + cols;
     if (row_tiles * col_tiles > (int64_t)0x7FFFFFFF) return FP4Q_ERR_SHAPE;
-    if (codes && (code_pitch < joined || code_pitch >= 2 * kDimLimit)) return FP4Q_ERR_SHAPE;
-    if (codes_t && (code_t_pitch < rows || code_t_pitch >= 2 * kDimLimit)) return FP4Q_ERR_SHAPE;
-    if (y_codes_t && (y_t_pitch < rows || y_t_pitch >= 2 * kDimLimit)) return FP4Q_ERR_SHAPE;
+    if (codes && (code_pitch < joined || code_pitch >= 4 * kLimit)) return FP4Q_ERR_SHAPE;
+    if (codes_t && (code_t_pitch < rows || code_t_pitch >= 4 * kLimit)) return FP4Q_ERR_SHAPE;
+    if (y_codes_t && (y_t_pitch < rows || y_t_pitch >= 4 * kLimit)) return FP4Q_ERR_SHAPE;
     if ((dtype != FP4Q_OUT_F32 && dtype != FP4Q_OUT_BF16) || bad_act(act) ||
         (format != FP4Q_E4M3 && format != FP4Q_E5M2))
         return FP4Q_ERR_ARG;

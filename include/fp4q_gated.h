@@ -74,7 +74,7 @@ int fp4q_gated8(const uint8_t *a, int64_t a_pitch, int a_format, const float *a_
  *                        second projection's weight gradient
  * Each is what fp4q_quantize8 makes of the fp32 tensor.  Each pair may be NULL, not all
  * three.  gate and up must be finite where their results count.  rows >= 0, 1 <= cols;
- * rows, cols < 2^27. */
+ * rows, cols < 2^23, pitches < 2^25. */
 int fp4q_gated8_backward(const void *dy, const void *gate, const void *up, int64_t rows, int64_t cols,
                          int dtype, int act, int format, uint8_t *codes, int64_t code_pitch,
                          float *scales, uint8_t *codes_t, int64_t code_t_pitch, float *scales_t,

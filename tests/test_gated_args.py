@@ -253,7 +253,8 @@ def grad(dy=G, gate=2 * G, up=3 * G, rows=4, cols=200, dtype=1, act=0, fmt=1, co
 
 @fake_addresses
 @pytest.mark.parametrize("change,want", [
-    ({"rows": -1}, SHAPE), ({"cols": 0}, SHAPE), ({"cols": 1 << 27}, SHAPE), ({"rows": 1 << 27}, SHAPE), ({"pitch": 448}, SHAPE),
+    ({"rows": -1}, SHAPE), ({"cols": 0}, SHAPE), ({"cols": 1 << 23}, SHAPE), ({"rows": 1 << 23}, SHAPE), ({"pitch": 448}, SHAPE),
+    ({"pitch": 1 << 25}, SHAPE), ({"pitch_t": 1 << 25}, SHAPE), ({"y_pitch": 1 << 25}, SHAPE),
     ({"pitch_t": 0}, SHAPE), ({"y_pitch": 0}, SHAPE), ({"dtype": 2}, ARG), ({"act": 4}, ARG), ({"fmt": 2}, ARG),
     ({"rows": 0, "dy": None}, OK), ({"dy": None}, NULL), ({"gate": None}, NULL), ({"up": None}, NULL), ({"scales": None}, NULL),
     ({"scales_t": None}, NULL), ({"y_scales": None}, NULL),
