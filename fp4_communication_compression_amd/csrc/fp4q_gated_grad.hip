@@ -3,9 +3,15 @@
 //
 //   dgate = dy up act'(gate),  dup = dy act(gate),  and y = act(gate) up again
 //
-// One pass over the three tensors: a workgroup holds a 128 x 128 tile of each result in
-// registers, 8 x 8 elements a thread, and writes dgate and dup along rows and along columns
-// and y along columns.  Bound by HBM: 6 bytes read and 5 written per bf16 element.
+// One pass over the three tensors: a workgroup of 512 threads holds a 128 x 128 tile of each
+// result, 4 x 8 elements a thread, and writes dgate and dup along rows and along columns and y
+// along columns.  A scale needs its 128 elements before their first code, and the tile is what
+// gives both orders theirs with the tensors read once.  Bound by HBM: 6 bytes read and 5 written
+// per bf16 element.  8192 x 11008 bf16, all three orders: silu 212 us, 4.7 TB/s of these bytes
+// (a large copy reaches 5.2), gelu_tanh 230, gelu 232; 2047 x 2752 gelu_tanh 23 us.
+//
+// 512 threads, not 256 of 8 x 8: 96 results a thread leave room for four wavefronts a SIMD, that
+// is for one workgroup to load while the other computes.
 #include "fp4q_act.h"
 #include "fp4q_f8.h"
 
@@ -16,6 +22,14 @@ using namespace fp4q_act;
 
 constexpr int kRows = 4, kThreads = kGroup / kRows * 16;  // rows of a thread; 8 columns
 constexpr int kWaves = kThreads / kWave;
+// Rows of the inputs under way at once: with all four the registers do not last, and fewer than
+// two leave the loads' latency open (2 against 4: 2048 x 4096 fp32 28.9 us and 30.5, 8192 x 11003
+// bf16 274 and 288; 3: 8192 x 11008 251 us against 241).
+constexpr int kAhead = 2;
+// Quads of y that a thread keeps in LDS, not registers, until the scales are there: 4 wavefronts a
+// SIMD leave a thread 128 registers, and what does not fit would go through memory (8192 x 11008:
+// 212 us against 241 with none aside, and 575 MB written where the codes are 460).
+constexpr int kAside = 3;
 enum { kGate, kUp, kY, kTensors };
 
 // One order of codes: rows are the rows of the joined tensor, or its columns.
@@ -58,6 +72,7 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2) void gated_grad_k
         unsigned turn[kTensors][kGroup * kGroup / 4];     // then the columns' codes
     } room;
     __shared__ Scale scales[kTensors][kGroup];
+    __shared__ float4 aside[kAside][kThreads];
     const int t = threadIdx.x, lane = t & (kWave - 1), wave = t / kWave, across = t & 15, down = t >> 4;
     const int tc = (int)(blockIdx.x % (unsigned)a.col_tiles), tr = (int)(blockIdx.x / (unsigned)a.col_tiles);
     const int row = tr * kGroup, col = tc * kGroup, r0 = row + kRows * down, c0 = col + 8 * across;
@@ -71,30 +86,37 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2) void gated_grad_k
     const int64_t joined = (int64_t)second + a.cols;
 
     float v[kTensors][kRows][8];
-    Eight<T> dy[kRows], gate[kRows], up[kRows];
-#pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-        const int left = r0 + i < a.rows ? a.cols - c0 : 0;
+    Eight<T> dy[kAhead], gate[kAhead], up[kAhead];
+    auto load = [&](int i) {
+        const int left = r0 + i < a.rows ? a.cols - c0 : 0, to = i % kAhead;
         const unsigned at = ((unsigned)(kRows * down + i) * (unsigned)a.cols + 8 * across) * (unsigned)sizeof(T);
-        dy[i].template load<kWhole>(of_tile(a.dy, at), left);
-        gate[i].template load<kWhole>(of_tile(a.gate, at), left);
-        up[i].template load<kWhole>(of_tile(a.up, at), left);
-    }
+        dy[to].template load<kWhole>(of_tile(a.dy, at), left);
+        gate[to].template load<kWhole>(of_tile(a.gate, at), left);
+        up[to].template load<kWhole>(of_tile(a.up, at), left);
+    };
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) load(i);
     const int64_t along = row * a.along.pitch + col;
     float *const gate_scales = a.along.scales + (int64_t)tc * a.rows + row;
     float *const up_scales = gate_scales + (int64_t)a.col_tiles * a.rows;
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
         float d[8], g[8], u[8];
-        dy[i].get(d);
-        gate[i].get(g);
-        up[i].get(u);
+        dy[i % kAhead].get(d);
+        gate[i % kAhead].get(g);
+        up[i % kAhead].get(u);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const Value f = activate<kAct>(g[j]);
             v[kGate][i][j] = d[j] * u[j] * f.slope;
             v[kUp][i][j] = d[j] * f.act;
             v[kY][i][j] = f.act * u[j];
+        }
+        if (i + kAhead < kRows) load(i + kAhead);
+#pragma unroll
+        for (int k = 2 * i; k < 2 * i + 2; ++k) {
+            const float *q = v[kY][i] + 4 * (k % 2);
+            if (k < kAside) aside[k][t] = make_float4(q[0], q[1], q[2], q[3]);
         }
         if (a.along.codes) {
             const int r = kRows * down + i;
@@ -104,6 +126,12 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2) void gated_grad_k
         }
     }
     if (!a.across.codes && !a.y.codes) return;
+#pragma unroll
+    for (int k = 0; k < kAside; ++k) {  // a thread's own: no barrier
+        const float4 q = aside[k][t];
+        float *const to = v[kY][k / 2] + 4 * (k % 2);
+        to[0] = q.x, to[1] = q.y, to[2] = q.z, to[3] = q.w;
+    }
 
     // The columns' largest magnitudes: over a thread's rows, then over the four rows of 16
     // lanes: an exchange of two registers between rows leaves one's maximum over two rows in
