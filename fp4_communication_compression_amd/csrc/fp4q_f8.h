@@ -1,5 +1,6 @@
 // fp4q_f8.h -- device and host helpers shared by the 8-bit linear-layer kernels
-// (fp4q_norm.hip, fp4q_quant8.hip, fp4q_gemm8.hip): element types, 8-bit scales
+// (fp4q_norm.hip, fp4q_quant8.hip, fp4q_gemm8.hip) and the gated
+// operators' (fp4q_gated8.hip, fp4q_gated_grad.hip, fp4q_gemv4.hip): element types, 8-bit scales
 // and codes, reductions over lanes, argument checks.
 #pragma once
 
