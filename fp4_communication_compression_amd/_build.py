@@ -13,7 +13,7 @@ SOURCES = [os.path.join(HERE, "csrc", n)
                      "fp4q_quant8.hip", "fp4q_gemv4.hip")]
 HEADERS = [*(os.path.join(ROOT, "include", n) for n in ("fp4q.h", "fp4q_linear.h", "fp4q_gated.h")),
            *(os.path.join(HERE, "csrc", n) for n in ("fp4q_numerics.h", "fp4q_f8.h", "fp4q_act.h", "fp4q_gemm8_plan.h",
-                                                     "fp4q_gemm8_tile.h", "fp4q_gated8_plan.h"))]
+                                                     "fp4q_gemm8_tile.h", "fp4q_gated8_plan.h", "fp4q_gemv4_plan.h"))]
 LIB = os.path.join(HERE, "libfp4q.so")
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

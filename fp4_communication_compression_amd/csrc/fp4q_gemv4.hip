@@ -26,17 +26,17 @@
 
 #include "fp4q_act.h"
 #include "fp4q_f8.h"
+#include "fp4q_gemv4_plan.h"
 
 namespace {
 
 using namespace fp4q_f8;
 using namespace fp4q_act;
+using namespace fp4q_few_plan;
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
-
-constexpr int kBlock = FP4Q_BLOCK, kStrip = 16;
 
 struct Payload {
     const uint8_t *codes, *micro;
@@ -212,6 +212,7 @@ struct Turn {
     unsigned micro[64];
     float scale[16];
 };
+static_assert(sizeof(Turn) == kTurnBytes, "what the plan counts");
 // (other types' views of them, which the compiler has to keep in order with the stores)
 typedef uint16_t AnyHalf __attribute__((may_alias));
 typedef f32x4 AnyQuad __attribute__((may_alias));
@@ -447,64 +448,26 @@ int check_sizes(int64_t M, int64_t K, int dtype, uint32_t flags) {
     if (flags & ~(uint32_t)FP4Q_FLAG_NO_FWHT) return FP4Q_ERR_ARG;
     return dtype == FP4Q_OUT_F32 || dtype == FP4Q_OUT_BF16 ? FP4Q_OK : FP4Q_ERR_ARG;
 }
-// Transformed bf16 x takes one part where out is bf16: 11 bits of values that come from 8.
-int parts_of(int dtype, int out_dtype, uint32_t flags) {
-    return dtype == FP4Q_OUT_F32 || (!(flags & FP4Q_FLAG_NO_FWHT) && out_dtype == FP4Q_OUT_F32) ? 2 : 1;
-}
-
-// Whether every workgroup makes x ready itself, which saves a launch, for as many blocks of 256
-// of x as its wavefronts do while the weight's first loads are on their way (one that has to be
-// transformed counts twice).  us, payloads from HBM, the other way in brackets: one row of 11008
-// 10.1 (13.3), two 11.7 (13.9); 8 rows of 4096 with two payloads of 11008 rows 20.0 (20.8), with
-// one of 4096 rows 10.5 (10.0); 4 transformed rows of 4096 10.6 (10.5), 5 12.9 (11.7).
-constexpr int kStageBlocks = 128, kLds = 160 * 1024;
-int64_t staged_bytes(int64_t cols, int64_t K) { return cols * (2 * (K + 8) + 4 * (K / kBlock)); }
-bool staged(int64_t M, int64_t K, int parts, uint32_t flags) {
-    const int64_t cols = M * parts, rest = 16 * (2 * 2 * cols * 64 + (int64_t)sizeof(Turn));  // of the widest kernel
-    const int64_t work = M * (K / kBlock) * (flags & FP4Q_FLAG_NO_FWHT ? 1 : 2);
-    return cols <= 16 && work <= kStageBlocks && staged_bytes(cols, K) + rest <= kLds;
-}
-size_t workspace_of(int64_t M, int64_t K, int parts, uint32_t flags) {
-    return staged(M, K, parts, flags) ? 0 : (size_t)(M * parts * (2 * K + 4 * (K / kBlock)));
-}
-
 template <int kWaves, int kCols, int kStrips, int kBlocksAhead, bool kGated, Source kSource>
-int run_kernel(Gemv4Args &p, int most, void *stream) {
-    const int each = 16 * kCols / p.parts;
-    void *args[] = {&p};
-    const int64_t units = ceil_div(p.N, kGated ? kStrip : kStrip * kStrips), chunks = ceil_div(p.M, each);
-    const dim3 grid((unsigned)std::min<int64_t>(units, most), (unsigned)chunks);
+int run_kernel(Gemv4Args &p, const Plan &plan, void *stream) {
     static_assert(kLimitM / 16 <= 65535, "chunks");
-    const int64_t cols = std::min<int64_t>(each, p.M) * p.parts;
-    const int64_t lds = kWaves * (2 * kStrips * cols * 64 + (int64_t)sizeof(Turn)) +
-                        (kSource == Source::kStaged ? staged_bytes(p.M * p.parts, p.K) : 0);
+    void *args[] = {&p};
+    const dim3 grid((unsigned)plan.groups, (unsigned)plan.chunks);
     const hipError_t e = hipLaunchKernel((const void *)&gemv4_kernel<kWaves, kCols, kStrips, kBlocksAhead, kGated, kSource>,
-                                         grid, dim3(kWaves * kWave), args, (size_t)lds, (hipStream_t)stream);
+                                         grid, dim3(kWaves * kWave), args, (size_t)plan.lds, (hipStream_t)stream);
     return e == hipSuccess ? FP4Q_OK : FP4Q_ERR_LAUNCH;
 }
-// The kernel and the number of its workgroups, one or two a CU.  Measured (us, payloads from
-// HBM; the other way in brackets):
-//   x made ready in the kernel: 16 wavefronts for one row of long K, 4096 x 11008 10.1 (8 of them:
-//   12.3), and for more than 32 blocks of x; else 8, two workgroups a CU: 1024 x 1024 3.7 (4.6),
-//   11008 x 4096 gated 13.7 (15.5)
-//   x in registers where 16 wavefronts have a block each: 16 x 32768 x 4096 22.5 (24.9 without
-//   the second block's loads ahead); gated, where two strips leave no registers for those, with
-//   more than one unit a workgroup: 16 x 11008 x 4096 22.6 (27.5), but 16 x 2752 14.3 (13.5)
-//   two strips, which share x, for two column tiles: 64 x 4096 x 4096 19.0 (30.8 with one); one
-//   strip, and more workgroups, for one: 16 x 4096 x 11008 21.8 (24.1)
-constexpr int kCus = 256;
 template <bool kGated>
-int run_product(Gemv4Args &p, bool stage, void *stream) {
+int run_product(Gemv4Args &p, const Plan &plan, void *stream) {
     constexpr int kS = kGated ? 2 : 1;
-    const int64_t cols = (int64_t)p.M * p.parts, blocks = p.K / kBlock;
-    if (stage) {
-        if ((!kGated && blocks > 16) || p.M * blocks > 32) return run_kernel<16, 1, kS, 1, kGated, Source::kStaged>(p, kCus, stream);
-        return run_kernel<8, 1, kS, 1, kGated, Source::kStaged>(p, 2 * kCus, stream);
+    switch (plan.way) {
+        case Way::kStaged:
+            if (plan.waves == 16) return run_kernel<16, 1, kS, 1, kGated, Source::kStaged>(p, plan, stream);
+            return run_kernel<8, 1, kS, 1, kGated, Source::kStaged>(p, plan, stream);
+        case Way::kHeld: return run_kernel<16, 1, kS, 3 - kS, kGated, Source::kOne>(p, plan, stream);
+        case Way::kLoaded: return run_kernel<8, 1, kS, 1, kGated, Source::kMemory>(p, plan, stream);
+        default: return run_kernel<8, 2, 2, 1, kGated, Source::kMemory>(p, plan, stream);
     }
-    if (cols <= 16 && blocks <= 16 && (!kGated || p.N > kStrip * kCus))
-        return run_kernel<16, 1, kS, 3 - kS, kGated, Source::kOne>(p, kCus, stream);
-    if (cols <= 16) return run_kernel<8, 1, kS, 1, kGated, Source::kMemory>(p, kCus, stream);
-    return run_kernel<8, 2, 2, 1, kGated, Source::kMemory>(p, kCus, stream);
 }
 
 int run(const void *x, int dtype, int64_t M, const Payload &w, const Payload *up, int64_t N, int64_t K, int act,
@@ -544,7 +507,8 @@ int run(const void *x, int dtype, int64_t M, const Payload &w, const Payload *up
         p.x = to;
         p.down = down;
     }
-    return up ? run_product<true>(p, !need, stream) : run_product<false>(p, !need, stream);
+    const Plan plan = plan_of(M, N, K, parts, flags, up != nullptr);
+    return up ? run_product<true>(p, plan, stream) : run_product<false>(p, plan, stream);
 }
 
 }  // namespace

@@ -2,9 +2,9 @@
 library's hipcc flags): libfp4q_instr_check.so (exhaustive sweeps of the
 kernels' rounding primitives, for tests/test_gpu_instructions.py),
 libfp4q_twins.so (compute-free traffic twins of the kernels, for bench.py's
-ceilings leg), libfp4q_gemm8_plan.so and libfp4q_gated8_plan.so (host code only:
-which kernel a product runs on, for tests/test_gemm_plan.py and
-tests/test_gated_plan.py)."""
+ceilings leg), libfp4q_gemm8_plan.so, libfp4q_gated8_plan.so and
+libfp4q_gemv4_plan.so (host code only: which kernel a product runs on, for
+tests/test_gemm_plan.py, tests/test_gated_plan.py and tests/test_gemv4_plan.py)."""
 from __future__ import annotations
 
 import os
@@ -14,7 +14,8 @@ import sys
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(os.path.dirname(HERE))
 LIBS = {"libfp4q_instr_check.so": "fp4q_instr_check.hip", "libfp4q_twins.so": "fp4q_twins.hip",
-        "libfp4q_gemm8_plan.so": "fp4q_gemm8_plan.hip", "libfp4q_gated8_plan.so": "fp4q_gated8_plan.hip"}
+        "libfp4q_gemm8_plan.so": "fp4q_gemm8_plan.hip", "libfp4q_gated8_plan.so": "fp4q_gated8_plan.hip",
+        "libfp4q_gemv4_plan.so": "fp4q_gemv4_plan.hip"}
 
 
 def build() -> list:
