@@ -30,6 +30,8 @@
  *   FP4Q_ACT_GELU       g (1 + erf(g / sqrt 2)) / 2
  *   FP4Q_ACT_GELU_TANH  g (1 + tanh(sqrt(2 / pi) (g + 0.044715 g^3))) / 2
  *   FP4Q_ACT_RELU       max(g, 0), with derivative 0 at 0
+ * At an infinite g they and their derivatives take their limits.  A factor 1 / (1 + exp(-g)) (or
+ * its like) that lies below 2^-126 may count as 0.
  */
 #ifndef FP4Q_GATED_H
 #define FP4Q_GATED_H
@@ -73,8 +75,9 @@ int fp4q_gated8(const uint8_t *a, int64_t a_pitch, int a_format, const float *a_
  *                        y_t_pitch, and scales [ceil(rows/128) x cols]: the operand of the
  *                        second projection's weight gradient
  * Each is what fp4q_quantize8 makes of the fp32 tensor.  Each pair may be NULL, not all
- * three.  gate and up must be finite where their results count.  rows >= 0, 1 <= cols;
- * rows, cols < 2^23, pitches < 2^25. */
+ * three.  The products are taken from left to right, and one that leaves fp32's range on the way
+ * is infinite: it, and a gate of +infinity in dup and y, give their blocks NaN scales.
+ * rows >= 0, 1 <= cols; rows, cols < 2^23, pitches < 2^25. */
 int fp4q_gated8_backward(const void *dy, const void *gate, const void *up, int64_t rows, int64_t cols,
                          int dtype, int act, int format, uint8_t *codes, int64_t code_pitch,
                          float *scales, uint8_t *codes_t, int64_t code_t_pitch, float *scales_t,
