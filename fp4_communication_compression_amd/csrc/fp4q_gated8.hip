@@ -156,7 +156,7 @@ __global__ __launch_bounds__(kWaves *kWave) void gated_strip_kernel(GatedArgs p)
         const auto rows = rows_at(p.b, (int64_t)n0 + (strip ? p.second : 0), here, w_pitch, wide);
         to.codes[0] = __builtin_amdgcn_raw_buffer_load_b128(rows, w_at, kb * kGroup, 0);
         to.codes[1] = __builtin_amdgcn_raw_buffer_load_b128(rows, w_at8, kb * kGroup, 0);
-        // (an item that does not exist takes any scale: its codes are zeros, but for a NaN's sake its own unit's)
+        // (a block or a unit that does not exist has zero codes and a zero scale)
         const int tile = min(n0, p.N - 1) / kGroup + (strip ? tiles / 2 : 0);
         to.scale = here > 0 ? p.sb[(int64_t)min(kb, blocks - 1) * tiles + tile] : 0.0f;
     };
@@ -219,6 +219,8 @@ __global__ __launch_bounds__(kWaves *kWave) void gated_strip_kernel(GatedArgs p)
             for (int c = 0; c < kCols; ++c) {
                 part.codes[c].low = keep_bytes(part.codes[c].low, end - 16 * quarter);
                 part.codes[c].high = keep_bytes(part.codes[c].high, end - 16 * quarter - 64);
+                // a block that does not exist: a's last one's scale was read, and 0 times an infinity is not 0
+                part.scale[c] = end > 0 ? part.scale[c] : 0.0f;
             }
 #pragma unroll
             for (int s = 0; s < 2; ++s) {

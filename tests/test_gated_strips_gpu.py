@@ -1,0 +1,26 @@
+"""The gated product of few rows: scales that are not finite."""
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from tests import linear_ref as ref
+from tests.test_gated_gpu import operands
+from tests.test_linear_gpu import fp4q  # noqa: F401 (the fixture)
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("m,n,k", [(1, 33, 100), (5, 300, 300), (16, 4113, 640), (20, 300, 200), (40, 70, 1100), (300, 200, 300)])
+def test_a_scale_that_is_infinite(fp4q, m, n, k):
+    """An infinite scale of a's last block makes its row's products infinite, with the block's sign,
+    in strips (whose wavefronts share K, some with a block less) as in tiles."""
+    a, sa, w, sw = operands(m, n, k, seed=7)
+    last = (k - 1) // 128 * 128
+    codes, p = w.view(torch.uint8), ref.groups(n) * 128
+    for half in (codes[:n, last:k], codes[p:, last:k]):
+        half.copy_((half & 0x3F) | 1)         # positive, and not zero
+    a.view(torch.uint8)[m - 1, last:k] = 0x38   # 1
+    sa[-1, m - 1] = float("inf")
+    got = fp4q.fp4q_gated8(a, sa, w, sw, "relu", want_pre=True)
+    for t in (got.gate, got.up, got.y):
+        assert bool((t[m - 1] == float("inf")).all()) and bool(t[:m - 1].isfinite().all())
