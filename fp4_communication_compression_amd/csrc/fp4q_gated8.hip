@@ -118,7 +118,7 @@ __device__ __forceinline__ u32x4 keep_bytes(u32x4 w, int keep) {
 template <int kFmtA, int kFmtW, int kWaves, int kCols>
 __global__ __launch_bounds__(kWaves *kWave) void gated_strip_kernel(GatedArgs p) {
     __shared__ u32x4 turn[kWaves][16 * 8];  // chunk c of row r at chunk c ^ (r / 2 & 7)
-    extern __shared__ float sums_room[];         // two units' [kWaves][2][M][16]
+    extern __shared__ float sums_room[];    // a unit's [kWaves][2][M][16], or two units' in turn
     const int lane = threadIdx.x & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int row16 = lane & 15, quarter = lane >> 4;
@@ -336,13 +336,13 @@ int fp4q_gated8(const uint8_t *a, int64_t a_pitch, int a_format, const float *a_
     p.up = up;
     void *args[] = {&p};
     if (plan.way == Way::kStrip) {
-        // (M = 64: two units' sums of 8 wavefronts take 128 KiB of LDS)
         const int waves = M <= 32 ? 16 : 8;
         const void *fn = M <= 16 ? Strip<16, 1>::get(a_format, w_format)
                          : M <= 32 ? Strip<16, 2>::get(a_format, w_format) : Strip<8, 4>::get(a_format, w_format);
-        const int64_t units = ceil_div(N, kStripOut);
+        // one unit's sums where no workgroup has a second one: always with more than 16 rows (plan_of)
+        const int64_t units = ceil_div(N, kStripOut), places = units > kCus ? 2 : 1;
         const hipError_t e = hipLaunchKernel(fn, dim3((unsigned)(units < kCus ? units : kCus)), dim3(waves * kWave), args,
-                                             (size_t)(2 * waves * 2 * M * 16 * 4), (hipStream_t)stream);
+                                             (size_t)(places * waves * 2 * M * 16 * 4), (hipStream_t)stream);
         return e == hipSuccess ? FP4Q_OK : FP4Q_ERR_LAUNCH;
     }
     const void *fn = nullptr;

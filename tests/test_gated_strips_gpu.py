@@ -1,13 +1,30 @@
-"""The gated product of few rows: scales that are not finite."""
+"""The gated product of few rows: several units of 16 outputs a workgroup, and scales that are not
+finite."""
 import pytest
 
 torch = pytest.importorskip("torch")
 
+from tests import gated_shapes
 from tests import linear_ref as ref
-from tests.test_gated_gpu import operands
+from tests.test_gated_gpu import E4M3, E5M2, check_gated, halves, operands
 from tests.test_linear_gpu import fp4q  # noqa: F401 (the fixture)
 
 pytestmark = pytest.mark.gpu
+STRIP = (64, 16, 1)
+
+
+@pytest.mark.parametrize("shape", [(16, 4113, 1111), (7, 11008, 640), (1, 8209, 2300), (13, 4097, 4096), (2, 12290, 129)])
+@pytest.mark.parametrize("fmt", [E4M3, E5M2])
+def test_several_units_a_workgroup(fp4q, shape, fmt):
+    """More units than the 256 workgroups: two or three each, the last ones fewer, whose sums take
+    the two halves of their LDS in turn."""
+    print(shape, fmt, flush=True)
+    m, n, k = shape
+    assert gated_shapes.plan(m, n, k) == STRIP and (n + 15) // 16 > 256
+    ops = operands(m, n, k, fmt, fmt)
+    got = fp4q.fp4q_gated8(*ops, "silu", want_pre=True)
+    check_gated(got, halves(*ops), "silu", True)
+    assert torch.equal(got.y, fp4q.fp4q_gated8(*ops, "silu").y)
 
 
 @pytest.mark.parametrize("m,n,k", [(1, 33, 100), (5, 300, 300), (16, 4113, 640), (20, 300, 200), (40, 70, 1100), (300, 200, 300)])
