@@ -8,8 +8,8 @@
 // operations on them, and neither g nor u need be written and read again.
 //
 // Tiles are bound as fp4q_gemm8's, by loads, LDS reads and scaled additions beside the matrix
-// cores: 8192 x 11008, K = 4096, with g and u 740 us, 1990 TFLOP/s (of a tile's 69 us 11.5 are its
-// beginning, the activation and three outputs); 2047 x 2752 53 us, 1741 TFLOP/s.  Strips are bound
+// cores: 8192 x 11008, K = 4096, with g and u 740 to 744 us, 1985 to 1995 TFLOP/s (of a tile's 69 us 11.5 are its
+// beginning, the activation and three outputs); 2047 x 2752 53 to 54 us, 1719 to 1741 TFLOP/s.  Strips are bound
 // by HBM: one row, 11008 x 4096 19.2 us, 4.7 TB/s of the weights (a large copy reaches 5.2).
 #include "fp4q_act.h"
 #include "fp4q_gated8_plan.h"

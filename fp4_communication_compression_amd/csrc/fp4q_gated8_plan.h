@@ -29,7 +29,8 @@ struct Plan {
 // among them, cost start_us; fitted to the times of every tile with 1 to 6 runs over 13 products
 // (48 x 11008 to 8192 x 11008, K = 4096 and 11008) and to the tiles' alone with every CU full.
 // Over those products the choice takes 3 % longer than the best way on average, 11 % at most
-// (128 x 2752, K = 11008).  At K = 4096: 2047 x 2752 57.8 us in 192-row tiles (256 rows 67.4, 128
+// (128 x 2752, K = 11008).  At K = 4096, in the series of the fit (the first one takes 53 us now, the
+// second 740, the third 24): 2047 x 2752 57.8 us in 192-row tiles (256 rows 67.4, 128
 // x 64 71.4, 64 x 64 81.0), 8192 x 11008 756 in 256-row tiles (827, 900, 1097), 48 x 11008 26.5 in
 // 64 x 64 tiles and two or four runs (32 x 64 29.2, whole 32.3).  Runs of K are added by a second
 // launch.

@@ -7,11 +7,13 @@
 // result, 4 x 8 elements a thread, and writes dgate and dup along rows and along columns and y
 // along columns.  A scale needs its 128 elements before their first code, and the tile is what
 // gives both orders theirs with the tensors read once.  Bound by HBM: 6 bytes read and 5 written
-// per bf16 element.  8192 x 11008 bf16, all three orders: silu 212 us, 4.7 TB/s of these bytes
-// (a large copy reaches 5.2), gelu_tanh 230, gelu 232; 2047 x 2752 gelu_tanh 23 us.
+// per bf16 element.  8192 x 11008 bf16, all three orders: silu 214 us, 4.6 TB/s of these bytes
+// (a large copy reaches 5.2), over cards gelu_tanh 221 to 231, gelu 225 to 236; 2047 x 2752
+// gelu_tanh 23 us.
 //
 // 512 threads, not 256 of 8 x 8: 96 results a thread leave room for four wavefronts a SIMD, that
-// is for one workgroup to load while the other computes.
+// is for one workgroup to load while the other computes.  (Not so fp32 relu: 129 or 130 registers,
+// one workgroup a CU; 2048 x 4096 28.8 us, silu 27.5.)
 #include "fp4q_act.h"
 #include "fp4q_f8.h"
 

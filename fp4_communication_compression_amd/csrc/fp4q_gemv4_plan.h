@@ -19,9 +19,10 @@ inline int parts_of(int dtype, int out_dtype, uint32_t flags) {
 
 // Whether every workgroup makes x ready itself, which saves a launch, for as many blocks of 256
 // of x as its wavefronts do while the weight's first loads are on their way (one that has to be
-// transformed counts twice).  us, payloads from HBM, the other way in brackets: one row of 11008
-// 10.1 (13.3), two 11.7 (13.9); 8 rows of 4096 with two payloads of 11008 rows 20.0 (20.8), with
-// one of 4096 rows 10.5 (10.0); 4 transformed rows of 4096 10.6 (10.5), 5 12.9 (11.7).
+// transformed counts twice).  us, payloads from HBM, the other way in brackets, in one series when
+// the rule was made (the first takes 9.1 now): one row of 11008 10.1 (13.3), two 11.7 (13.9); 8
+// rows of 4096 with two payloads of 11008 rows 20.0 (20.8), with one of 4096 rows 10.5 (10.0); 4
+// transformed rows of 4096 10.6 (10.5), 5 12.9 (11.7).
 constexpr int kStageBlocks = 128;
 inline int64_t staged_bytes(int64_t cols, int64_t K) { return cols * (2 * (K + 8) + 4 * (K / kBlock)); }
 inline bool staged(int64_t M, int64_t K, int parts, uint32_t flags) {
@@ -44,13 +45,15 @@ struct Plan {
     int waves, tiles, each;
     int64_t chunks, unit, groups, lds;
 };
-// One or two workgroups a CU.  Measured (us, payloads from HBM; the other way in brackets):
+// One or two workgroups a CU.  Measured (us, payloads from HBM; the other way in brackets), in the
+// series of the rule above:
 //   x made ready in the kernel: 16 wavefronts for one row of long K, 4096 x 11008 10.1 (8 of them:
 //   12.3), and for more than 32 blocks of x; else 8, two workgroups a CU: 1024 x 1024 3.7 (4.6),
 //   11008 x 4096 gated 13.7 (15.5)
 //   x in registers where 16 wavefronts have a block each: 16 x 32768 x 4096 22.5 (24.9 without
-//   the second block's loads ahead); gated, where two strips leave no registers for those, with
-//   more than one unit a workgroup: 16 x 11008 x 4096 22.6 (27.5), but 16 x 2752 14.3 (13.5)
+//   the second block's loads ahead); gated, where two strips leave no registers for those (and
+//   spill 9 of 128 as it is, 40 bytes of scratch a lane), with more than one unit a workgroup:
+//   16 x 11008 x 4096 22.6 (27.5), but 16 x 2752 14.3 (13.5)
 //   two strips, which share x, for two column tiles: 64 x 4096 x 4096 19.0 (30.8 with one); one
 //   strip, and more workgroups, for one: 16 x 4096 x 11008 21.8 (24.1)
 inline Plan plan_of(int64_t M, int64_t N, int64_t K, int parts, uint32_t flags, bool gated) {

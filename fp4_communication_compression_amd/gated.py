@@ -196,7 +196,7 @@ def fp4q_gemv4(x, weight, flags: int = 0, out=None, out_dtype=None, stream=None)
     """x [M, K] (float32 or bfloat16) times the transpose of a weight [N, K] held as a
     payload (codes, micro-scales, block scales), as ``fp4q_compress`` with the same
     ``flags`` makes it -> [M, N] in x's type, ``out_dtype`` or ``out``'s.  Made for few
-    rows: its time is that of reading the payload."""
+    rows: its time is that of reading the payload, once for every 32 of them or fewer."""
     kind, M, K = _rows_in(x)
     N, codes, micro, block = _payload(weight, "weight", K)
     code, dtype = _few_rows(x, out, out_dtype, N, flags)

@@ -84,8 +84,9 @@ int fp4q_gated8_backward(const void *dy, const void *gate, const void *up, int64
                          uint8_t *y_codes_t, int64_t y_t_pitch, float *y_scales_t, void *stream);
 
 /* out[m][n] = sum over k of x[m][k] W[n][k], where W [N x K] is a payload: what
- * fp4q_decompress makes of it in exact arithmetic.  Made for few rows of x (its time is that
- * of reading the payload); any number is taken.
+ * fp4q_decompress makes of it in exact arithmetic.  Made for few rows of x: its time is that
+ * of reading the payload, once for all of up to 16 columns (rows of x times their parts, below),
+ * else once for every 32.  Any number is taken.
  *   x           [M x K] of `dtype`
  *   codes, micro_scales, block_scales   W as fp4q_compress_ex makes it; K % 256 == 0
  *   flags       FP4Q_FLAG_NO_FWHT for a payload made with that flag.  Otherwise W is
@@ -97,8 +98,8 @@ int fp4q_gated8_backward(const void *dy, const void *gate, const void *up, int64
  * (2^98 at most) for each row and block of 256: bf16 x exactly, but for values 2^-28 below
  * the block's largest; fp32 or transformed x in two parts, to 2^-22 of each value (and
  * 2^-39 of the block's largest), but for transformed bf16 x with bf16 out, which takes one
- * part, to 2^-11 (x itself has 8 bits, and so has out).  Products are exact and added in fp32 by the matrix core, a
- * block's sum times its scale in fp32.  As for fp4q_compress, x must be finite with
+ * part, to 2^-11 (x itself has 8 bits, and so has out; fp32 out takes two).  Products are exact and
+ * added in fp32 by the matrix core, a block's sum times its scale in fp32.  As for fp4q_compress, x must be finite with
  * |x| < 2^118, which is not checked (a row of x that is not gives a row of out that is not);
  * of x what lies below 2^-112, and of a block's sum what lies below 2^-126 before its scale
  * (times 2^17), may be dropped.
